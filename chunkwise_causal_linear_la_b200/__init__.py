@@ -15,6 +15,11 @@ this package is its Python binding:
     from chunkwise_causal_linear_la_b200.autograd import chunk_linear_attention
     o = chunk_linear_attention(q, k, v, gamma, phi="elu1", normalize=True)
 
+    # softmax-attention layers of a hybrid stack: store the new tokens, then attend over the cache
+    k_cache, v_cache, k_scale, v_scale = kv_cache(n_pages, 64, H_kv, 128, torch.float8_e4m3fn)
+    la_kv_write(k, v, k_cache, v_cache, page_table, kv_len, k_scale=k_scale, v_scale=v_scale)
+    o, _ = la_paged_attn(q, k_cache, v_cache, page_table, kv_len, k_scale=k_scale, v_scale=v_scale)
+
 ``workloads`` draws the seeded synthetic inputs of the standard workloads.
 """
 from .binding import (  # noqa: F401
@@ -40,10 +45,16 @@ from .binding import (  # noqa: F401
     la_fwd_gated_delta,
     la_fwd_gated_delta_chunk,
     gated_delta_workspace_size,
+    kv_cache,
+    la_kv_read,
+    la_kv_write,
     la_norm_gate,
+    la_paged_attn,
     la_step,
     la_step_gated,
     la_step_norm,
     load_library,
+    paged_attn_path,
+    paged_attn_workspace_size,
     workspace_size,
 )

@@ -8,6 +8,7 @@ the library is missing this module raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -26,6 +27,8 @@ LA_FLAG_TEST_WAIT_TIMEOUT = 0x100  # tests of the failure path only (see include
 _PHI = {"identity": LA_PHI_IDENTITY, "elu1": LA_PHI_ELU1, LA_PHI_IDENTITY: LA_PHI_IDENTITY,
         LA_PHI_ELU1: LA_PHI_ELU1}
 _DT = {torch.float32: LA_F32, torch.bfloat16: LA_BF16}
+LA_KV_BF16, LA_KV_E4M3, LA_KV_INT8 = 0, 1, 2
+_KV = {torch.bfloat16: LA_KV_BF16, torch.float8_e4m3fn: LA_KV_E4M3, torch.int8: LA_KV_INT8}
 
 # Every function include/la_b200.h declares.
 EXPORTS = ("la_fwd_chunk", "la_fwd_chunk_z", "la_fwd_chunk_gated", "la_fwd_chunk_workspace_size", "la_step",
@@ -34,7 +37,8 @@ EXPORTS = ("la_fwd_chunk", "la_fwd_chunk_z", "la_fwd_chunk_gated", "la_fwd_chunk
            "la_fwd_gated_delta", "la_fwd_gated_delta_chunk", "la_fwd_gated_delta_workspace_size",
            "la_fwd_chunk_path", "la_fwd_chunk_host", "la_fwd_chunk_host_arena_size", "la_bwd_chunk_gated",
            "la_bwd_chunk_norm", "la_bwd_chunk_norm_workspace_size", "la_bwd_chunk_gated_norm",
-           "la_bwd_chunk_gated_norm_workspace_size")
+           "la_bwd_chunk_gated_norm_workspace_size", "la_kv_write", "la_kv_read", "la_paged_attn",
+           "la_paged_attn_workspace_size", "la_paged_attn_path")
 
 
 class LaTensor(ctypes.Structure):
@@ -43,6 +47,15 @@ class LaTensor(ctypes.Structure):
         ("dtype", ctypes.c_int32),
         ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("D", ctypes.c_int64),
         ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+    ]
+
+
+class LaKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("format", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("H", ctypes.c_int64), ("D", ctypes.c_int64),
+        ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64),
     ]
 
 
@@ -119,6 +132,17 @@ def load_library(path: str = LIB_PATH):
     lib.la_device_error.restype = i32
     lib.la_fwd_chunk_noalloc.argtypes = [P, P, P, vp, vp, i64, i32, i32, i32, P, vp, i32, vp]
     lib.la_fwd_chunk_noalloc.restype = i32
+    C = ctypes.POINTER(LaKvCache)
+    lib.la_kv_write.argtypes = [P, P, vp, i64, C, vp, i64, vp, vp]
+    lib.la_kv_write.restype = i32
+    lib.la_kv_read.argtypes = [C, vp, i64, vp, vp, i64, P, P, vp]
+    lib.la_kv_read.restype = i32
+    lib.la_paged_attn.argtypes = [P, C, vp, i64, vp, vp, i64, ctypes.c_float, i64, P, vp, i32, vp, sz, vp]
+    lib.la_paged_attn.restype = i32
+    lib.la_paged_attn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32, i64, i64, i32, i32, i32]
+    lib.la_paged_attn_workspace_size.restype = sz
+    lib.la_paged_attn_path.argtypes = [i64, i64, i64, i64, i32, i32, i32]
+    lib.la_paged_attn_path.restype = i32
     _lib = lib
     return lib
 
@@ -562,3 +586,167 @@ def la_fwd_gated_delta_chunk(q, k, v, g, beta, cu_seqlens=None, initial_state=No
                                       _stream(stream))
     _check(lib, st, "la_fwd_gated_delta_chunk")
     return out, final_state
+
+
+# ---------------------------------------------------------------- paged cache
+def kv_cache(n_pages, page_size, H, D, dtype=torch.bfloat16, device="cuda"):
+    """An empty paged cache (see la_kv_cache in include/la_b200.h): k and v pages
+    [n_pages, page_size, H, D] of dtype bfloat16, float8_e4m3fn or int8, and for the 8-bit ones
+    their scales float32 [n_pages, H, page_size] (None for bfloat16).  Memory is not initialised.
+    Returns (k_cache, v_cache, k_scale, v_scale)."""
+    if dtype not in _KV:
+        raise TypeError("cache dtype %s not supported (bfloat16, float8_e4m3fn or int8)" % dtype)
+    k, v = (torch.empty((n_pages, page_size, H, D), dtype=dtype, device=device) for _ in range(2))
+    if dtype == torch.bfloat16:
+        return k, v, None, None
+    ks, vs = (torch.empty((n_pages, H, page_size), dtype=torch.float32, device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+def describe_cache(k, v, k_scale=None, v_scale=None) -> LaKvCache:
+    """la_kv_cache for [n_pages, page_size, H, D] pages of keys and values (D contiguous, the other
+    axes in any order, the same strides for both) and their [n_pages, H, page_size] scales."""
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, H, D] tensors of one shape")
+    if k.dtype not in _KV or v.dtype != k.dtype:
+        raise TypeError("k_cache and v_cache must share one dtype: bfloat16, float8_e4m3fn or int8")
+    n, p, H, D = k.shape
+    strides = [(k.stride(i), v.stride(i)) for i in range(3) if k.shape[i] > 1]
+    if (D > 1 and (k.stride(3) != 1 or v.stride(3) != 1)) or any(a != b for a, b in strides):
+        raise ValueError("k_cache and v_cache must have equal strides and a contiguous head dim")
+    eight = k.dtype != torch.bfloat16
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not eight and t is not None:
+            raise TypeError("%s: a bfloat16 cache has no scales" % name)
+        if eight and (t is None or t.dtype != torch.float32 or tuple(t.shape) != (n, H, p) or not t.is_contiguous()):
+            raise TypeError("%s must be a contiguous float32 [n_pages, H, page_size] tensor" % name)
+    return LaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if eight else None,
+                     v_scale.data_ptr() if eight else None, _KV[k.dtype], n, p, H, D, k.stride(0), k.stride(1),
+                     k.stride(2))
+
+
+def _on_current_device(**tensors):
+    """The calls launch on the current device, in its current stream: tensors of another one are refused."""
+    for name, t in tensors.items():
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+            raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+
+
+def _allocating_for(stream):
+    """Outputs and workspace made for a call on `stream` belong to that stream in torch's allocator, so
+    that their memory is not handed to other work before the call has run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _index(name, t, shape):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise TypeError("%s must be a contiguous int32 tensor of shape %s" % (name, list(shape)))
+    return None if t is None else t.data_ptr()
+
+
+def _n_seqs(B, cu_seqlens):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise TypeError("cu_seqlens must hold n_seqs + 1 entries")
+    return cu_seqlens.numel() - 1
+
+
+def _table(page_table, n):
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise TypeError("page_table must be [n_seqs, max_pages]")
+    return _index("page_table", page_table, tuple(page_table.shape)), page_table.shape[1]
+
+
+def la_kv_write(k, v, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_scale=None, v_scale=None,
+                stream=None):
+    """Store the new tokens' keys and values in a paged cache, quantised where it is an 8-bit one
+    (see la_kv_write in include/la_b200.h).  k, v [B,T,H,D]; page_table int32 [N, max_pages]; kv_len
+    int32 [N], the new tokens counted; cu_seqlens int32 [N+1] or None."""
+    lib = load_library()
+    n = _n_seqs(k.shape[0], cu_seqlens)
+    cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
+    tk, tv, tl, tc = describe(k), describe(v), _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
+    _on_current_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                       page_table=page_table, kv_len=kv_len, cu_seqlens=cu_seqlens)
+    st = lib.la_kv_write(ctypes.byref(tk), ctypes.byref(tv), tc, n, ctypes.byref(cache), table, max_pages, tl,
+                         _stream(stream))
+    _check(lib, st, "la_kv_write")
+
+
+def la_kv_read(k_cache, v_cache, page_table, T, start=None, cu_seqlens=None, k_scale=None, v_scale=None,
+               dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Read cached rows back (see la_kv_read in include/la_b200.h): T positions of each of the N
+    sequences from start[n] on (int32 [N]; None: from 0), or with cu_seqlens int32 [N+1] a packed batch
+    of T rows.  Returns (k [B,T,H,D], v [B,T,H,D]) of the given dtype."""
+    lib = load_library()
+    n = page_table.shape[0] if cu_seqlens is None else _n_seqs(1, cu_seqlens)
+    cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
+    shape = (n if cu_seqlens is None else 1, int(T), k_cache.shape[2], k_cache.shape[3])
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s" % (name, list(shape)))
+    ts, tc = _index("start", start, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
+    _on_current_device(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+                       start=start, cu_seqlens=cu_seqlens, k_out=k_out, v_out=v_out)
+    with _allocating_for(stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
+    tk, tv = describe(k_out), describe(v_out)
+    st = lib.la_kv_read(ctypes.byref(cache), table, max_pages, ts, tc, n, ctypes.byref(tk), ctypes.byref(tv),
+                        _stream(stream))
+    _check(lib, st, "la_kv_read")
+    return k_out, v_out
+
+
+def paged_attn_workspace_size(B, T, H, D, n_seqs, varlen, H_kv, page_size, cache_dtype=torch.bfloat16,
+                              dtype=torch.bfloat16, flags=0) -> int:
+    """Bytes of workspace la_paged_attn needs (0: none)."""
+    n = load_library().la_paged_attn_workspace_size(B, T, H, D, n_seqs, int(bool(varlen)), H_kv, page_size,
+                                                    _KV[cache_dtype], _DT[dtype], flags)
+    if n == ctypes.c_size_t(-1).value:
+        raise LaError(LA_ERR_INVALID_ARG, "la_paged_attn_workspace_size rejected the arguments")
+    return int(n)
+
+
+def paged_attn_path(H, D, H_kv, page_size, cache_dtype=torch.bfloat16, dtype=torch.bfloat16, flags=LA_FLAG_NONE) -> int:
+    """Kernel la_paged_attn runs for this shape: LA_PATH_TENSOR_CORE, LA_PATH_CUDA_CORE, or -1."""
+    return int(load_library().la_paged_attn_path(H, D, H_kv, page_size, _KV[cache_dtype], _DT[dtype], flags))
+
+
+def la_paged_attn(q, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_scale=None, v_scale=None, scale=None,
+                  window=0, out=None, lse=None, return_lse=False, flags=LA_FLAG_NONE, workspace=None, stream=None):
+    """Causal softmax attention of the new tokens over the paged cache that holds them already
+    (see la_paged_attn in include/la_b200.h).  q [B,T,H,D]; kv_len int32 [N]; scale: D^-1/2 if None;
+    window: 0 or the positions a query sees.  Returns (out, lse float32 [B,T,H] or None)."""
+    lib = load_library()
+    tq = describe(q)
+    B, T, H, D = q.shape
+    n = _n_seqs(B, cu_seqlens)
+    cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
+    tl, tc = _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, T, H) or not lse.is_contiguous()):
+        raise TypeError("lse must be a contiguous float32 [B, T, H] tensor")
+    _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, kv_len=kv_len,
+                       page_table=page_table, cu_seqlens=cu_seqlens, out=out, lse=lse, workspace=workspace)
+    need = paged_attn_workspace_size(B, T, H, D, n, cu_seqlens is not None, cache.H, cache.page_size, k_cache.dtype,
+                                     q.dtype, flags)
+    with _allocating_for(stream):
+        if out is None:
+            out = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    to = describe(out)
+    st = lib.la_paged_attn(ctypes.byref(tq), ctypes.byref(cache), table, max_pages, tl, tc, n,
+                           float(D ** -0.5 if scale is None else scale), int(window), ctypes.byref(to),
+                           None if lse is None else lse.data_ptr(), int(flags),
+                           None if workspace is None else workspace.data_ptr(),
+                           0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(lib, st, "la_paged_attn")
+    return out, lse

@@ -89,6 +89,40 @@ struct DeltaArgs {
   bool test_wait_timeout = false;  // LA_FLAG_TEST_WAIT_TIMEOUT (chunked path)
 };
 
+// Paged cache as the kernels see it (la_kv_cache).
+struct KvView {
+  uint8_t *k, *v;
+  float *ks, *vs;  // [n_pages][H][page_size], 8-bit formats
+  int format;      // la_kv_format
+  int64_t n_pages;
+  int page_size, H, D;
+  int64_t s_page, s_tok, s_head;  // element strides
+  const int32_t *table;           // [n_seqs][max_pages]
+  int64_t max_pages;
+};
+
+struct KvMoveArgs {  // la_kv_write, la_kv_read
+  KvView c;
+  TensorView k, v;            // the dense rows
+  const int32_t *cu_seqlens;  // NULL for dense batches
+  const int32_t *pos;         // write: kv_len; read: first position (NULL: zeros)
+  int64_t B, T, n_seqs;
+  int dtype;
+};
+
+struct PagedArgs {  // la_paged_attn
+  KvView c;
+  TensorView q;
+  void *out;
+  int64_t o_sb, o_st, o_sh;
+  float *lse;  // NULL, or [B][T][H]
+  const int32_t *cu_seqlens, *kv_len;
+  int64_t B, T, n_seqs;
+  int H, dtype;
+  float scale;
+  int window;  // 0: none
+};
+
 // Sets the calling thread's la_last_error() message and returns `status`.
 la_status report_error(la_status status, const char *msg);
 
@@ -124,6 +158,11 @@ cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t stream);
 // One-token decode step.
 bool step_supported(const StepArgs &a);
 cudaError_t launch_step(const StepArgs &a, cudaStream_t stream);
+
+// Paged cache: rows in and out, and attention over it on the CUDA cores.
+cudaError_t launch_kv_write(const KvMoveArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvMoveArgs &a, cudaStream_t stream);
+cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t stream);
 
 // Tensor-core (tcgen05 / TMA / TMEM) chunked forward for bf16.
 bool tc_supported(const ChunkArgs &a);

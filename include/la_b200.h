@@ -528,6 +528,138 @@ LA_API la_status la_bwd_chunk_gated_norm(const la_tensor *q, const la_tensor *k,
                                          void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Softmax attention over a paged cache: la_kv_write, la_kv_read, la_paged_attn.
+ * (Additions of this library.  "1.6 长上下文与高效注意力" describes hybrid stacks that
+ * keep a few softmax-attention layers between linear-attention ones; those
+ * layers keep their keys and values in a cache that grows with the sequence,
+ * where la_step's layers keep a state.  These calls are their la_fwd_chunk and
+ * la_step: one call takes a prompt, a piece of a prompt, a few drafted tokens or
+ * a single token of every sequence.)
+ */
+
+/* How a cache holds a row (the D values of one token and head).  The 8-bit
+ * formats keep one scale per row, a power of two, so that code * scale is exact
+ * in bf16: s = 2^e, the smallest with max |x| <= qmax s and e >= -126, and
+ * code = x / s rounded to nearest even (qmax 448 for e4m3, 127 for int8; e4m3
+ * without infinities, as NVIDIA and OCP define it).  A row that holds an
+ * infinity or a NaN gets a NaN scale and codes of zero: it reads back as NaN. */
+typedef enum { LA_KV_BF16 = 0, LA_KV_E4M3 = 1, LA_KV_INT8 = 2 } la_kv_format;
+
+/*
+ * A paged cache: n_pages pages of page_size tokens in device memory.
+ *   k, v        pages of keys and values, [n_pages, page_size, H, D] each, in the
+ *               format's element type; 16-byte aligned, D contiguous
+ *   k_scale, v_scale  float[n_pages, H, page_size], contiguous, 16-byte aligned
+ *               (8-bit formats; NULL for LA_KV_BF16)
+ *   stride_*    element strides of the page, token and head axes, shared by k
+ *               and v, multiples of 16 bytes, positive wherever the axis has
+ *               more than one entry; any order of the axes (token by token, or
+ *               head by head inside a page).  Rows must not overlap.
+ * Position p of sequence n lives in slot p % page_size of page
+ * page_table[n][p / page_size].  An entry of the table outside [0, n_pages)
+ * stands for a missing page: nothing is written to it and it reads as zeros.
+ */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int32_t format;
+  int64_t n_pages, page_size, H, D;
+  int64_t stride_page, stride_token, stride_head;
+} la_kv_cache;
+
+/*
+ * la_kv_write -- quantise the new tokens' keys and values into the cache.
+ *   k, v        [B, T, H, D] each, one dtype (bf16 or f32), H and D the cache's.
+ *   cu_seqlens, n_seqs  dense or packed batch, as for la_fwd_chunk.
+ *   cache       destination.  LA_KV_BF16 rounds f32 rows to nearest even.
+ *   page_table  device int32[n_seqs, max_pages], contiguous.
+ *   kv_len      device int32[n_seqs]: tokens each sequence has in the cache
+ *               after this call, the new ones among them.  Token i of a sequence's
+ *               L new tokens is stored at position kv_len[n] - L + i; a position
+ *               that is negative, past max_pages * page_size or in a missing page is
+ *               skipped.
+ * No other byte of the cache changes.  Two tokens of one call that map to the
+ * same slot (a page that two sequences' new tokens share) race: one is kept,
+ * possibly mixed with the other.  Head dims {16, 32, 64, 128, 256}.
+ *
+ * la_kv_read -- read a range of positions back as [B, T, H, D] rows.
+ *   start       device int32[n_seqs] or NULL (zeros): token i of sequence n is read
+ *               from position start[n] + i.  A position outside the table or in a
+ *               missing page reads as zeros.  The caller keeps the range inside
+ *               what was stored: other slots return what the memory holds.
+ *   k_out, v_out  [B, T, H, D], one dtype (bf16 or f32); written for every token
+ *               that belongs to a sequence (others are left untouched).
+ *
+ * Both are one pass over memory.  Errors: LA_ERR_INVALID_ARG for NULL or misaligned
+ * pointers, inconsistent shapes, dtypes or strides, an unknown format;
+ * LA_ERR_UNSUPPORTED for other head dims or more than 2^31 - 1 rows;
+ * LA_ERR_CUDA if a launch fails.  A problem without tokens returns LA_OK.
+ */
+LA_API la_status la_kv_write(const la_tensor *k, const la_tensor *v, const int32_t *cu_seqlens, int64_t n_seqs,
+                             const la_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                             const int32_t *kv_len, void *stream);
+LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                            const int32_t *start, const int32_t *cu_seqlens, int64_t n_seqs,
+                            const la_tensor *k_out, const la_tensor *v_out, void *stream);
+
+/*
+ * la_paged_attn -- causal softmax attention of a chunk of new tokens over the
+ * cache (the new tokens' own keys and values are in it already: la_kv_write
+ * first).  Query i of sequence n's L new tokens stands at position
+ * p = kv_len[n] - L + i and sees the positions j with
+ *     max(0, p - window + 1) <= j <= p   (window 0: 0 <= j <= p),
+ *     o = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j).
+ *   q, out      [B, T, H, D], one dtype (bf16 or f32); H a multiple of the cache's
+ *               heads: query head h reads cache head h / (H / cache.H).
+ *   cache, page_table, max_pages, kv_len, cu_seqlens, n_seqs  as for la_kv_write.
+ *               Positions past max_pages * page_size are not seen; a missing page
+ *               inside the range is seen as rows of zeros.
+ *   scale       positive factor of the scores (D^-1/2 usually).
+ *   window      0, or the number of positions a query sees, itself included.
+ *   out         written for every token that belongs to a sequence (others are
+ *               left untouched); a query that sees nothing (p < 0) gives zeros.
+ *   lse         NULL, or device float[B, T, H]; -infinity where nothing is seen.
+ *   flags       LA_FLAG_NONE, or LA_FLAG_SIMT for the CUDA-core kernel.
+ *   workspace   device scratch of at least la_paged_attn_workspace_size(...)
+ *               bytes (NULL allowed when that is 0), 256-byte aligned; need not be
+ *               initialised.  Calls whose work may overlap on the GPU (two streams,
+ *               two captured graphs) need a workspace each.
+ * Slots that no query of the call sees may hold anything, NaN included, with
+ * one exception: in a LA_KV_BF16 cache the values (v) at positions below
+ * kv_len[n] must be finite where a query of the sequence does not see them but
+ * sees another position of the same 128.  A position that a query does see takes
+ * part as the formula says, infinities and NaN too.
+ * Reads of the cache follow 64-bit offsets; page_table, kv_len and cu_seqlens
+ * are read on the device only and their values are never trusted with an
+ * address: no value of theirs makes the call read or write out of bounds.
+ *
+ * Kernels: bf16 with D 64 or 128, page_size a multiple of 8, at most 128 query
+ * heads a cache head and q strides that are not zero run on the tensor cores;
+ * every other shape, f32 and LA_FLAG_SIMT on the CUDA cores, in fp32.
+ * la_paged_attn_path tells (as la_fwd_chunk_path does; -1: rejected).
+ *
+ * Arithmetic: 8-bit rows enter as the bf16 values they stand for (a scale that
+ * is not a power of two is rounded to bf16 first on the tensor cores); scores,
+ * softmax statistics and outputs are accumulated in fp32; on the tensor cores the
+ * softmax weights are rounded to bf16 for the product with v; out is rounded once.
+ * Results do not depend on other sequences of the call beyond fp32 rounding: where
+ * a sequence's keys are split over CTAs depends on the whole call.
+ *
+ * Errors: as la_kv_write, and LA_ERR_INVALID_ARG for a scale that is not positive
+ * and finite, a negative window, unknown flags; LA_ERR_WORKSPACE for a missing or
+ * small workspace; LA_ERR_CUDA if a launch fails.
+ */
+LA_API size_t la_paged_attn_workspace_size(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs,
+                                           int32_t has_cu_seqlens, int64_t H_kv, int64_t page_size,
+                                           int32_t format, int32_t dtype, int32_t flags);
+LA_API int32_t la_paged_attn_path(int64_t H, int64_t D, int64_t H_kv, int64_t page_size, int32_t format,
+                                  int32_t dtype, int32_t flags);
+LA_API la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int32_t *page_table,
+                               int64_t max_pages, const int32_t *kv_len, const int32_t *cu_seqlens, int64_t n_seqs,
+                               float scale, int64_t window, const la_tensor *out, float *lse, int32_t flags,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * la_fwd_chunk_noalloc -- la_fwd_chunk for callers that cannot allocate device
  * memory.  (An addition of this library; the pages have no counterpart.)
  *
