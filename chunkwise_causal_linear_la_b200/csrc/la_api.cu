@@ -301,12 +301,13 @@ int32_t la_version(void) { return 1 * 10000 + 0 * 100 + 0; }
 
 la_status la_device_error(uint32_t *flags, uint32_t *detail, int32_t reset) {
   if (!flags || !detail) return fail(LA_ERR_INVALID_ARG, "flags and detail must not be NULL");
-  unsigned int f = 0, w = 0, f2 = 0, w2 = 0;
+  unsigned int f = 0, w = 0, f2 = 0, w2 = 0, f3 = 0, w3 = 0;
   cudaError_t err = tc_device_error(&f, &w, reset != 0);
   if (err == cudaSuccess) err = gdn_device_error(&f2, &w2, reset != 0);
+  if (err == cudaSuccess) err = pa_device_error(&f3, &w3, reset != 0);
   if (err != cudaSuccess) return fail(LA_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(err));
-  *flags = f | f2;
-  *detail = w ? w : w2;
+  *flags = f | f2 | f3;
+  *detail = w ? w : w2 ? w2 : w3;
   return ok();
 }
 

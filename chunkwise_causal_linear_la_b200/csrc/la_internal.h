@@ -164,6 +164,20 @@ cudaError_t launch_kv_write(const KvMoveArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvMoveArgs &a, cudaStream_t stream);
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t stream);
 
+// Attention over the paged cache on the tensor cores, on a fixed grid of CTAs that
+// share the work out among themselves (one per SM of a B200; none waits for another).
+constexpr int kPagedCtas = 148;
+bool pa_tc_shape(int64_t H, int64_t D, int64_t H_kv, int64_t page_size);
+bool pa_tc_supported(const PagedArgs &a);
+size_t pa_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs, bool packed, int64_t H_kv,
+                          int ctas);
+cudaError_t launch_paged_tc(const PagedArgs &a, int ctas, void *workspace, cudaStream_t stream, const char **why);
+cudaError_t pa_device_error(unsigned int *flags, unsigned int *where, bool reset);
+
+// 4-D TMA map of bytes or bf16: sizes and box in elements, strides of the three outer axes in bytes.
+bool encode_map4(CUtensorMap *m, bool bytes, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                 const uint32_t (&box)[4], bool swizzle128);
+
 // Tensor-core (tcgen05 / TMA / TMEM) chunked forward for bf16.
 bool tc_supported(const ChunkArgs &a);
 bool tc_can_fuse_norm_gate(const ChunkArgs &a);

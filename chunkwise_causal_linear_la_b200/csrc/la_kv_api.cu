@@ -189,15 +189,17 @@ int32_t la_paged_attn_path(int64_t H, int64_t D, int64_t H_kv, int64_t page_size
   if (H <= 0 || H_kv <= 0 || H % H_kv || !head_dim_ok(D) || page_size <= 0 || page_size > 65536) return -1;
   if (format != LA_KV_BF16 && format != LA_KV_E4M3 && format != LA_KV_INT8) return -1;
   if ((dtype != LA_F32 && dtype != LA_BF16) || (flags & ~LA_FLAG_SIMT)) return -1;
-  return 2;
+  return dtype == LA_BF16 && !(flags & LA_FLAG_SIMT) && pa_tc_shape(H, D, H_kv, page_size) ? 1 : 2;
 }
 
 size_t la_paged_attn_workspace_size(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs,
                                     int32_t has_cu_seqlens, int64_t H_kv, int64_t page_size, int32_t format,
                                     int32_t dtype, int32_t flags) {
-  if (B < 0 || T < 0 || n_seqs < 0 || la_paged_attn_path(H, D, H_kv, page_size, format, dtype, flags) < 0)
+  const int32_t path = la_paged_attn_path(H, D, H_kv, page_size, format, dtype, flags);
+  if (B < 0 || T < 0 || n_seqs < 0 || path < 0 || !within(kMaxElems, B, T, H, D) || n_seqs > 0x7FFFFFFE)
     return (size_t)-1;
-  return 0;
+  if (path == 2 || B * T == 0 || n_seqs == 0) return 0;
+  return pa_workspace_bytes(B, T, H, D, n_seqs, has_cu_seqlens != 0, H_kv, kPagedCtas);
 }
 
 la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
@@ -241,8 +243,23 @@ la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int3
   a.dtype = q->dtype;
   a.scale = scale;
   a.window = window > 0x7FFFFFFF ? 0 : (int)window;  // positions are int32: a wider window hides nothing
-  (void)workspace_bytes;
-  const cudaError_t e = launch_paged_simt(a, (cudaStream_t)stream);
+  const size_t need = la_paged_attn_workspace_size(q->B, q->T, q->H, q->D, n_seqs, cu_seqlens != nullptr, cache->H,
+                                                   cache->page_size, cache->format, q->dtype, flags);
+  if (need == (size_t)-1) return fail(LA_ERR_UNSUPPORTED, "the batch is too large");
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(LA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  cudaError_t e;
+  if (need > 0 && pa_tc_supported(a)) {
+    int device = 0;
+    if ((e = bind_device(&device)) != cudaSuccess)
+      return fail(LA_ERR_CUDA, "cudaGetDevice / cudaSetDevice: %s", cudaGetErrorString(e));
+    const char *why = "";
+    e = launch_paged_tc(a, kPagedCtas, workspace, (cudaStream_t)stream, &why);
+    if (e != cudaSuccess)
+      return fail(LA_ERR_CUDA, "paged attention, tensor cores: %s%s%s", cudaGetErrorString(e), *why ? ": " : "", why);
+    return ok();
+  }
+  e = launch_paged_simt(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(LA_ERR_CUDA, "paged attention kernel: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -91,6 +91,18 @@ bool make_map(CUtensorMap *m, const TensorView &t, int64_t B, int64_t T, int64_t
   return r == CUDA_SUCCESS;
 }
 
+bool encode_map4(CUtensorMap *m, bool bytes, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                 const uint32_t (&box)[4], bool swizzle128) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
+  return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+             d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 __device__ unsigned int g_tc_error = 0;
 // First wait that gave up: 0x80000000 | chunk << 8 | barrier index.
 __device__ unsigned int g_tc_where = 0;

@@ -135,8 +135,26 @@ def test_paths_and_workspace(lib):
         assert b.paged_attn_workspace_size(1, 64, 16, 128, 1, False, 4, 16, **kw) == 0
     for H, D, Hkv, page in ((16, 32, 4, 16), (16, 256, 4, 16), (16, 128, 4, 20), (258, 64, 2, 16)):
         assert b.paged_attn_path(H, D, Hkv, page) == b.LA_PATH_CUDA_CORE
+    for H, D, Hkv, page in ((16, 64, 4, 16), (16, 128, 16, 8), (256, 128, 2, 200), (5, 64, 5, 48)):
+        for fmt in (torch.bfloat16, torch.float8_e4m3fn, torch.int8):
+            assert b.paged_attn_path(H, D, Hkv, page, fmt) == b.LA_PATH_TENSOR_CORE
     with pytest.raises(b.LaError):
         b.paged_attn_workspace_size(1, 64, 15, 128, 1, False, 4, 16)
+    # entries (32 bytes and an 8-byte prefix each) grow with the batch, the parts of 148 CTAs do not
+    small = b.paged_attn_workspace_size(1, 1, 16, 128, 1, False, 4, 16)
+    assert small >= 148 * 4 * 128 * (128 + 2) * 4
+    assert b.paged_attn_workspace_size(1, 1, 16, 64, 1, False, 4, 16) < small
+    many = b.paged_attn_workspace_size(1, 1 << 20, 16, 128, 1000, True, 4, 16)
+    assert many - small >= ((1 << 20) // 64 + 1000 - 1) * 40
+    assert b.paged_attn_workspace_size(1, 0, 16, 128, 1, False, 4, 16) == 0
+
+
+def test_attention_needs_its_workspace(lib):
+    from chunkwise_causal_linear_la_b200 import binding as b
+
+    need = b.paged_attn_workspace_size(1, 4, 4, 64, 1, False, 2, 16, torch.float8_e4m3fn)
+    assert _attn(lib) == b.LA_ERR_WORKSPACE and str(need).encode() in lib.la_last_error()
+    assert _attn(lib, ws=0x100000, wsb=need - 1) == b.LA_ERR_WORKSPACE
 
 
 def test_binding_refuses_what_it_cannot_describe():

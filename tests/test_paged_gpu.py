@@ -291,8 +291,12 @@ def test_dense_batch_with_strides(la, fmt):
 def test_broadcast_queries(la):
     """One query for every head (a zero head stride) takes the CUDA cores and gives the same."""
     c = Case([3], [50], 4, 2, 64, 16, BF, seed=3)
+    one = c.q[:, :1].cuda()
     c.q = c.q[:, :1].expand(-1, 4, -1)
-    out, lse = attn(la, c, c.fill(la, "cuda"))
+    k, v, _, _ = c.fill(la, "cuda")
+    out, lse = la.la_paged_attn(one.expand(-1, 4, -1)[None], k, v, c.table.cuda(),
+                                torch.tensor(c.kv_len, dtype=torch.int32, device="cuda"), cu_seqlens=c.cu.cuda(),
+                                return_lse=True)
     hold(c, out, lse, simt=True)
 
 
@@ -426,3 +430,18 @@ def test_long_contexts_of_single_tokens(la, fmt, H, Hkv, D, n, ctx):
     ctxs = [ctx, 3, 700][:n]
     c = Case([1] * n, ctxs, H, Hkv, D, 64, fmt, seed=13)
     hold(c, *attn(la, c, c.fill(la, "cuda")))
+
+
+@pytest.mark.parametrize("fmt", [BF, E4, I8])
+@pytest.mark.parametrize("lens,ctx,H,Hkv,D,page,window", [
+    ([1] * 40, [128 * (i % 7) + 37 * i for i in range(40)], 8, 8, 64, 16, 0),      # many short items a CTA
+    ([1, 90, 1, 33, 2], [4000, 700, 127, 3000, 2500], 16, 8, 128, 32, 0),          # both kinds of items, mixed
+    ([150, 70], [2100, 900], 6, 6, 64, 64, 0),                                      # two query tiles, cut items
+    ([140, 1, 9], [1500, 4000, 2048], 16, 16, 64, 16, 700),                         # under a window
+    ([300], [1800], 10, 2, 128, 128, 0),
+])
+def test_several_items_and_cut_ones_a_cta(la, lens, ctx, H, Hkv, D, page, window, fmt):
+    """More key tiles than CTAs: a CTA walks several entries, and entries are cut between CTAs anywhere."""
+    c = Case(lens, ctx, H, Hkv, D, page, fmt, seed=len(lens) + D, layout="head" if D == 64 else "token")
+    hold(c, *attn(la, c, c.fill(la, "cuda"), window=window), window=window)
+    assert la.device_error(reset=True) == (0, 0)
