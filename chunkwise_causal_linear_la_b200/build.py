@@ -52,9 +52,9 @@ def _stale() -> bool:
 TC_LAUNCH_REGS = 168
 # source file -> kernel whose launch register count is checked
 TC_KERNELS = {"la_tc.cu": "chunk_tc_kernel", "la_gdn.cu": "gdn_tc_kernel", "la_pa.cu": "pa_kernel"}
-# launch registers of instantiations with more threads, by a part of their mangled names: 512 threads have 128
-TC_OTHER_REGS = {"pa_kernelILi64ELi1E": 128, "pa_kernelILi128ELi1E": 128, "pa_kernelILi64ELi2E": 128,
-                 "pa_kernelILi128ELi2E": 128}
+# launch registers of instantiations with more threads, by a part of their mangled names: 896 threads have 72, 640 have 96
+TC_OTHER_REGS = {"pa_kernelILi%dELi%dELi%dE" % (d, f, n): 72 if n == 1 else 96
+                 for d in (64, 128) for f in (1, 2) for n in (1, 2)}
 
 
 def _check_tc_registers(ptxas_log: str, kernel: str, src: str) -> None:

@@ -57,7 +57,62 @@ __device__ unsigned int g_pa_where = 0;
 namespace {
 
 using namespace sm100;
-using namespace tcsync;
+using tcsync::drain_bar;
+using tcsync::pack2;
+using tcsync::Sync;
+
+// Up to 64 probes of a barrier, in as few instructions as they take: many warps wait here beside few that work, on
+// the same issue slots (a probe returns after some hundred cycles, not after its suspend hint).
+__device__ __forceinline__ bool mbar_probe(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 16;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 p, n, 0;\n\t@p bra AGAIN;\n\t"
+      "setp.ne.u32 p, n, n;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// tcsync::wait_bar by such probes; IDLE: by a warp that nobody waits for soon.
+template <bool IDLE = false>
+__device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile) {
+  uint64_t *b = sy.bar + idx;
+  if (mbar_test(b, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (IDLE) {
+      __nanosleep(200);
+      if (mbar_test(b, parity)) return true;
+    } else if (mbar_probe(b, parity)) {
+      return true;
+    }
+    if (*sy.abort) return false;
+    if (clock64() - t0 > tcsync::kTimeoutCycles) {
+      *sy.abort = 1;
+      atomicOr(sy.err, 1u);
+      atomicCAS(sy.where, 0u, 0x80000000u | ((uint32_t)(tile & 0x7FFFFF) << 8) | (uint32_t)idx);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+template <bool IDLE = false>
+__device__ __forceinline__ bool wait_on_warp(const Sync &sy, int idx, uint32_t parity, int tile) {
+  return __all_sync(0xffffffffu, wait_on<IDLE>(sy, idx, parity, tile));
+}
 
 constexpr int kTile = 128;  // keys of a tile, rows of a query tile
 
@@ -76,7 +131,7 @@ struct alignas(16) CtaWork {
 struct PaArgs {
   const int32_t *cu, *kv_len, *table;
   int64_t T, max_pages, n_pages, n_seqs;
-  int32_t page_size, box, g, tpt, Hkv, H, window;
+  int32_t page_size, box, g, tpt, per, Hkv, H, window;  // tokens of a query tile, of an entry
   int32_t e_max, G;
   int64_t cap;  // max_pages * page_size
   float c;      // scale * log2(e)
@@ -138,7 +193,7 @@ __device__ __forceinline__ void seq_span(const PaArgs &a, int64_t n, int64_t &st
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
   __shared__ int64_t ws[32];
   const int tid = threadIdx.x;
-  const int64_t per = 2 * a.tpt;  // tokens of an entry
+  const int64_t per = a.per;
   int64_t sum, carry = 0;
   for (int64_t n0 = 0; n0 < a.n_seqs; n0 += kPlanThreads) {
     const int64_t n = n0 + tid;
@@ -173,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       x.tok = (int)(st + t0);
       x.ntok = (int)max((int64_t)0, min(per, len - t0));
       const int64_t pos = kv - len + t0;
-      x.pos = (int)max(pos, -((int64_t)1 << 31));
+      x.pos = (int)max(pos, -((int64_t)1 << 30));  // below 0 all the same
       x.kv_end = (int)min(kv, a.cap);
       const int64_t end = min(pos + x.ntok, (int64_t)x.kv_end);
       const int64_t beg = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
@@ -214,18 +269,25 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
 }
 
 // ------------------------------------------------------------------ main kernel
-template <int D, int FMT>
+template <int D, int FMT, int NQ>
 struct PaCfg {
   static constexpr bool Q8 = FMT != LA_KV_BF16;
-  static constexpr int THREADS = Q8 ? 512 : 384;
+  static constexpr int CONV = Q8 ? (NQ == 1 ? 16 : 8) : 0;  // conversion warps
+  static constexpr int THREADS = 384 + 32 * CONV;
+  static constexpr int ROWS = NQ == 1 ? 64 : 128;    // rows of a query tile
+  static constexpr int WROWS = ROWS / 4;             // of them, a softmax warp's
   static constexpr int SLABS = D / 64;               // 64-column slabs of a bf16 tile
   static constexpr int SLAB = kTile * 128;           // bytes of one
   static constexpr int TILE = SLABS * SLAB;          // a bf16 operand tile
+  static constexpr int QSLAB = ROWS * 128;
+  static constexpr int QTILE = SLABS * QSLAB;
   static constexpr int RAW = kTile * D;              // a tile of codes
-  static constexpr int NS = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);  // operand slots (keys and values in turn)
-  static constexpr int NR = Q8 ? (D == 128 ? 3 : 8) : 0;                    // stages of codes
+  // operand slots and stages of codes, keys and values in turn: even numbers, so that the conversion warps of keys and
+  // those of values have slots and stages of their own
+  static constexpr int NS = (Q8 ? 4 : NQ == 1 ? 6 : 5) * (128 / D);
+  static constexpr int NR = Q8 ? (D == 128 ? (NQ == 1 ? 4 : 2) : NQ == 1 ? 8 : 6) : 0;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_OP = 2 * TILE;
+  static constexpr int OFF_OP = NQ * QTILE;
   static constexpr int OFF_RAW = OFF_OP + NS * TILE;
   static constexpr int OFF_SC = OFF_RAW + NR * RAW;  // scales of a stage, 128 floats
   static constexpr int OFF_ML = OFF_SC + NR * kTile * 4;
@@ -233,20 +295,25 @@ struct PaCfg {
   static constexpr int B_FULL = 0, B_EMPTY = NS, B_RFULL = 2 * NS, B_REMPTY = B_RFULL + NR, B_QFULL = B_REMPTY + NR,
                        B_QEMPTY = B_QFULL + 1, B_SFULL = B_QFULL + 2, B_PFULL = B_QFULL + 4, B_OFULL = B_QFULL + 6,
                        B_OEMPTY = B_QFULL + 8, B_MERGE = B_QFULL + 10, B_DRAIN = B_QFULL + 11,
-                       B_READY = B_QFULL + 12,  // bf16, per slot: fixed up
+                       B_PSPLIT = B_QFULL + 12, B_ODONE = B_QFULL + 14,  // one query tile: P of both groups; PV done
+                       B_READY = B_QFULL + 15,  // bf16, per slot: fixed up
                        NBAR = B_READY + (Q8 ? 0 : NS);
   // per item (mod 16) and fix-up or conversion warp: values that are not finite were taken out.  (A flag left
   // from 16 items before only costs a look for such values.)
   static constexpr int OFF_BAD = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;
   static constexpr int OFF_MISC = OFF_BAD + 16 * 16;
   static constexpr int SMEM_USED = OFF_MISC + 16;
-  static constexpr int SMEM_BYTES = SMEM_USED + 1024;
+  static constexpr int SMEM_BYTES = SMEM_USED;
   // tensor memory columns
   static constexpr int T_S = 0, T_O = 2 * kTile, T_COLS = 512;
   static_assert(T_O + 2 * D <= 512, "tensor memory");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
   // register split (per thread; shares add up to the launch's)
-  static constexpr int R_AUX = Q8 ? 56 : 104, R_SOFT = Q8 ? 192 : 200, R_CONV = 72;
+  static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
+  static constexpr int R_AUX = Q8 ? (NQ == 1 ? 72 : 80) : 104, R_SOFT = Q8 ? (NQ == 1 ? 112 : 136) : 200,
+                       R_CONV = NQ == 1 ? 48 : 64;
+  static_assert(R_AUX <= R_LAUNCH && R_CONV <= R_LAUNCH && R_SOFT >= R_LAUNCH, "setmaxnreg .dec and .inc");
+  static_assert(128 * R_AUX + 256 * R_SOFT + 32 * CONV * R_CONV <= THREADS * R_LAUNCH, "register split");
 };
 
 // A piece of an entry: `n` key tiles from tile t0 on, of one cache head.
@@ -287,11 +354,11 @@ struct Walk {
   }
 };
 
-// Positions that token `tk` of an entry sees: [lo, hi).
-__device__ __forceinline__ void sees(const PaArgs &a, const Entry &e, int tk, int64_t &lo, int64_t &hi) {
-  const int64_t p = (int64_t)e.pos + tk;
-  hi = min(p + 1, (int64_t)e.kv_end);
-  lo = a.window > 0 ? max((int64_t)0, p - a.window + 1) : 0;
+// Positions that token `tk` of an entry sees: [lo, hi).  (32 bits hold a position: kv_len is an int32.)
+__device__ __forceinline__ void sees(const PaArgs &a, const Entry &e, int tk, int &lo, int &hi) {
+  const int p = e.pos + tk;
+  hi = min(p + 1, e.kv_end);
+  lo = a.window > 0 ? max(0, p - (a.window - 1)) : 0;
 }
 
 // Of the keys of tile t: all tokens of the entry see those in [b, c); some those in
@@ -299,17 +366,13 @@ __device__ __forceinline__ void sees(const PaArgs &a, const Entry &e, int tk, in
 struct Reach {
   int a, b, c, d;
 };
+__device__ __forceinline__ int in_tile(int p, int ts) { return min(max(p - ts, 0), kTile); }
 __device__ __forceinline__ Reach reach(const PaArgs &a, const Entry &e, int t) {
-  int64_t lo0, hi0, lo1, hi1;
+  int lo0, hi0, lo1, hi1;
   sees(a, e, 0, lo0, hi0);
   sees(a, e, max(e.ntok, 1) - 1, lo1, hi1);
-  const int64_t ts = (int64_t)t * kTile;
-  Reach r;
-  r.a = (int)min(max(lo0 - ts, (int64_t)0), (int64_t)kTile);
-  r.b = (int)min(max(lo1 - ts, (int64_t)0), (int64_t)kTile);
-  r.c = (int)min(max(hi0 - ts, (int64_t)0), (int64_t)kTile);
-  r.d = (int)min(max(hi1 - ts, (int64_t)0), (int64_t)kTile);
-  return r;
+  const int ts = t * kTile;
+  return Reach{in_tile(lo0, ts), in_tile(lo1, ts), in_tile(hi0, ts), in_tile(hi1, ts)};
 }
 __device__ __forceinline__ bool partly(const Reach &r) { return r.b > 0 || r.c < kTile; }
 
@@ -319,27 +382,46 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two codes (byte positions picked by SEL) as bf16x2, times s2.
+// Sixteen codes times the scale f as bf16.
 //   e4m3: exponent and mantissa bits moved to bf16's places, value 2^-120 of the code's; the product with
-//         2^120 is exact (bf16 keeps subnormals), and so is the one with a power-of-two scale.
+//         2^120 is exact (bf16 keeps subnormals), and so is the one with a power-of-two scale.  For scales up to
+//         2^7 (2^120 f is a bf16 then) the two are one.
 //   int8: with the low 7 bits L and the sign bit S, (128 + L) - (128 + 128 S) by bit patterns of bf16.
+__device__ __forceinline__ uint32_t mul2(uint32_t v, __nv_bfloat162 f) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&v), f);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
 template <int FMT>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int hi, __nv_bfloat162 s2) {
-  uint32_t v;
-  __nv_bfloat162 r;
+__device__ __forceinline__ void convert16(const uint4 &w, float f, uint4 &o0, uint4 &o1) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t v[8];
   if (FMT == LA_KV_E4M3) {
-    const uint32_t x = __byte_perm(w, 0, hi ? 0x3424 : 0x1404);
-    v = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-    const uint32_t big = 0x7B807B80u;
-    r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&big));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = __byte_perm(in[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
+      v[k] = ((b >> 4) & 0x07F007F0u) | (b & 0x80008000u);
+    }
+    const bool wide = f > 128.f;
+    const __nv_bfloat162 f2 = __float2bfloat162_rn((wide ? 1.f : f) * 1.329227995784916e36f);  // 2^120
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], f2);
+    if (__any_sync(0xffffffffu, wide)) {
+      const __nv_bfloat162 g2 = __float2bfloat162_rn(wide ? f : 1.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], g2);
+    }
   } else {
-    const uint32_t x = __byte_perm(w, 0, hi ? 0x4342 : 0x4140);
-    v = (x & 0x007F007Fu) | 0x43004300u;
-    const uint32_t b = (x & 0x00800080u) | 0x43004300u;
-    r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = __byte_perm(in[k >> 1], 0, k & 1 ? 0x4342 : 0x4140);
+      const uint32_t p = (b & 0x007F007Fu) | 0x43004300u, q = (b & 0x00800080u) | 0x43004300u;
+      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&p), *reinterpret_cast<const __nv_bfloat162 *>(&q));
+      v[k] = mul2(*reinterpret_cast<const uint32_t *>(&r), f2);
+    }
   }
-  r = __hmul2(r, s2);
-  return *reinterpret_cast<uint32_t *>(&r);
+  o0 = make_uint4(v[0], v[1], v[2], v[3]);
+  o1 = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
 __device__ __forceinline__ bool finite_f(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
@@ -349,31 +431,35 @@ __device__ __forceinline__ uint32_t keep_finite(uint32_t w) {  // bf16x2
   return w;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__((PaCfg<D, FMT>::THREADS), 1)
+template <int D, int FMT, int NQ>
+__global__ void __launch_bounds__((PaCfg<D, FMT, NQ>::THREADS), 1)
 pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
           const __grid_constant__ CUtensorMap tm_v, const PaArgs a) {
-  using G = PaCfg<D, FMT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using G = PaCfg<D, FMT, NQ>;
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::OFF_BAR);
   float *sc = reinterpret_cast<float *>(sm + G::OFF_SC);
   float2 *ml = reinterpret_cast<float2 *>(sm + G::OFF_ML);
-  volatile int *bad = reinterpret_cast<volatile int *>(sm + G::OFF_BAD);
+  volatile uint8_t *bad = sm + G::OFF_BAD;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + G::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + G::OFF_MISC + 4);
   const Sync sy{bars, abort_flag, &g_pa_error, &g_pa_where};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (smem_u32(sm) & 1023) {  // the swizzled tiles need it (no static shared memory lies in front)
+    if (tid == 0) atomicOr(&g_pa_error, 4u);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t cnt = 1;
-      if (G::Q8 && i < G::NS) cnt = 4;                                  // FULL: conversion warps
+      if (G::Q8 && i < G::NS) cnt = G::CONV / 2;                        // FULL: conversion warps
       if (!G::Q8 && i >= G::B_EMPTY && i < G::B_EMPTY + G::NS) cnt = 3;  // products done, seen by the fix-up warps
-      if (i >= G::B_REMPTY && i < G::B_REMPTY + G::NR) cnt = 4;         // codes read
+      if (i >= G::B_REMPTY && i < G::B_REMPTY + G::NR) cnt = G::CONV / 2;  // codes read
       if (i >= G::B_PFULL && i < G::B_PFULL + 2) cnt = 4;               // softmax warps
       if (i >= G::B_OEMPTY && i < G::B_OEMPTY + 2) cnt = 4;
       if (i == G::B_MERGE) cnt = 4;
+      if (i >= G::B_PSPLIT && i < G::B_PSPLIT + 2) cnt = 8;
       if (i >= G::B_READY) cnt = 2;  // fix-up warps
       mbar_init(bars + i, cnt);
     }
@@ -402,7 +488,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       uint32_t seq = 0, items = 0;  // operand tiles and items started
       bool ok = true;
       while (ok && walk.next(a, it)) {
-        const bool two = it.e.ntok > a.tpt;
+        const bool two = NQ == 2 && it.e.ntok > a.tpt;
         // page of this lane's box in tile t
         auto page_at = [&](int t, int &slot) -> int {
           const int64_t p = (int64_t)t * kTile + lane * a.box;
@@ -424,7 +510,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             const CUtensorMap *tm = kvi ? &tm_v : &tm_k;
             if (!G::Q8) {
               const int s = seq % G::NS;
-              if (!(ok = wait_bar_warp(sy, G::B_EMPTY + s, ((seq / G::NS) & 1) ^ 1, it.t0 + i))) break;
+              if (!(ok = wait_on_warp(sy, G::B_EMPTY + s, ((seq / G::NS) & 1) ^ 1, it.t0 + i))) break;
               if (lane == 0) mbar_arrive_expect_tx(bars + G::B_FULL + s, G::TILE);
               __syncwarp();
               if (lane < nb) {
@@ -435,7 +521,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
               }
             } else {
               const int s = seq % (G::NR > 0 ? G::NR : 1);
-              if (!(ok = wait_bar_warp(sy, G::B_REMPTY + s, ((seq / (G::NR > 0 ? G::NR : 1)) & 1) ^ 1, it.t0 + i))) break;
+              if (!(ok = wait_on_warp(sy, G::B_REMPTY + s, ((seq / (G::NR > 0 ? G::NR : 1)) & 1) ^ 1, it.t0 + i))) break;
               const uint32_t have = __popc(__ballot_sync(0xffffffffu, pg >= 0));
               if (lane < nb && pg < 0)
                 for (int r = 0; r < a.box; ++r) sc[s * kTile + lane * a.box + r] = 0.f;
@@ -451,7 +537,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
               }
             }
             if (i == 0 && kvi == 0) {  // the item's queries, after its first keys are on their way
-              if (!(ok = wait_bar_warp(sy, G::B_QEMPTY, (items & 1) ^ 1, it.t0))) {
+              if (!(ok = wait_on_warp(sy, G::B_QEMPTY, (items & 1) ^ 1, it.t0))) {
                 ++seq;
                 break;
               }
@@ -459,7 +545,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                 mbar_arrive_expect_tx(bars + G::B_QFULL, two ? 2 * q_bytes : q_bytes);
                 for (int w = 0; w < (two ? 2 : 1); ++w)
                   for (int sl = 0; sl < G::SLABS; ++sl)
-                    tma_load_4d(sm + G::OFF_Q + w * G::TILE + sl * G::SLAB, &tm_q, bars + G::B_QFULL, sl * 64,
+                    tma_load_4d(sm + G::OFF_Q + w * G::QTILE + sl * G::QSLAB, &tm_q, bars + G::B_QFULL, sl * 64,
                                 it.head * a.g, it.e.tok + w * a.tpt, it.e.b);
               }
               ++items;
@@ -481,60 +567,109 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     } else if (warp == 1) {
       if (lane == 0) {
         // ---------------------------------------------------------- MMA issuer
-        constexpr uint32_t ID_QK = idesc_bf16_f32(kTile, kTile, 0, 0);
-        constexpr uint32_t ID_PV = idesc_bf16_f32(kTile, D, 0, 1);
+          constexpr uint32_t ID_QK = idesc_bf16_f32(G::ROWS, kTile, 0, 0);
+        constexpr uint32_t ID_PV = idesc_bf16_f32(G::ROWS, D, 0, 1);
         const uint64_t dq0 = smem_desc_sw128(smem_u32(sm + G::OFF_Q), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(op_slot(0)), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(op_slot(0)), G::SLAB, 1024);
-        uint32_t seq = 0, items = 0, used[2] = {0, 0}, pcnt[2] = {0, 0};
+        uint32_t seq = 0, items = 0, used[2] = {0, 0}, pcnt[2] = {0, 0}, bcnt[2] = {0, 0};
         bool ok = true;
+        // S[w] = Q[qt] K^T for the keys in slot sl
+        auto qk = [&](int w, int qt, uint32_t sl) {
+          tc_fence_after();
+          const uint64_t dq = dq0 + (uint64_t)(qt * (G::QTILE >> 4));
+          const uint64_t dk = dk0 + (uint64_t)(sl * (G::TILE >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            umma_bf16(tbase + G::T_S + w * kTile, dq + (((kk >> 2) * G::QSLAB + (kk & 3) * 32) >> 4),
+                      dk + (((kk >> 2) * G::SLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
+          }
+          umma_commit(bars + G::B_SFULL + w);
+        };
+        auto keys = [&](int i) -> bool {  // tile i's keys are in their slot
+          const uint32_t k = seq + 2 * i;
+          return wait_on(sy, G::B_FULL + k % G::NS, (k / G::NS) & 1, it.t0 + i);
+        };
+        auto values = [&](int i) -> bool {
+          const uint32_t k = seq + 2 * i + 1;
+          const bool fix = !G::Q8 && partly(reach(a, it.e, it.t0 + i));
+          return wait_on(sy, (fix ? G::B_READY : G::B_FULL) + k % G::NS, (k / G::NS) & 1, it.t0 + i);
+        };
+        auto o_free = [&](int w) -> bool {  // O[w] of the item before has been read
+          if (used[w] && !wait_on(sy, G::B_OEMPTY + w, (used[w] - 1) & 1, it.t0)) return false;
+          ++used[w];
+          return true;
+        };
         while (ok && walk.next(a, it)) {
-          const bool two = it.e.ntok > a.tpt;
-          const int ns = two ? 2 * it.n : it.n;
-          auto qk = [&](int s) -> bool {
-            const int w = s & 1, i = two ? s >> 1 : s;
-            const uint32_t k = seq + 2 * i, sl = k % G::NS;
-            if (!two || w == 0)
-              if (!wait_bar(sy, G::B_FULL + sl, (k / G::NS) & 1, it.t0 + i)) return false;
-            tc_fence_after();
-            const uint64_t dq = dq0 + (uint64_t)((two ? w : 0) * (G::TILE >> 4));
-            const uint64_t dk = dk0 + (uint64_t)(sl * (G::TILE >> 4));
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * G::SLAB + (kk & 3) * 32) >> 4;
-              umma_bf16(tbase + G::T_S + w * kTile, dq + off, dk + off, ID_QK, kk > 0);
-            }
-            umma_commit(bars + G::B_SFULL + w);
-            if (!two || w == 1) umma_commit(bars + G::B_EMPTY + sl);
-            if (s == ns - 1) umma_commit(bars + G::B_QEMPTY);
-            return true;
-          };
-          ok = wait_bar(sy, G::B_QFULL, items & 1, it.t0);
+          const bool two = NQ == 2 && it.e.ntok > a.tpt;
+          ok = wait_on(sy, G::B_QFULL, items & 1, it.t0);
           ++items;
-          ok = ok && qk(0) && (ns < 2 || qk(1));
-          for (int s = 0; s < ns && ok; ++s) {
-            const int w = s & 1, i = two ? s >> 1 : s;
-            const uint32_t k = seq + 2 * i + 1, sl = k % G::NS;
-            if (!two || w == 0) {
-              const bool fix = !G::Q8 && partly(reach(a, it.e, it.t0 + i));
-              if (!(ok = wait_bar(sy, (fix ? G::B_READY : G::B_FULL) + sl, (k / G::NS) & 1, it.t0 + i))) break;
+          if (two) {
+            // QK(0, K0) QK(1, K0), then for each tile and group w: PV(w, Vi), QK(w, Ki+1)
+            if (ok && (ok = keys(0))) {
+              qk(0, 0, seq % G::NS);
+              qk(1, 1, seq % G::NS);
+              umma_commit(bars + G::B_EMPTY + seq % G::NS);
+              if (it.n == 1) umma_commit(bars + G::B_QEMPTY);
             }
-            if (!(ok = wait_bar(sy, G::B_PFULL + w, pcnt[w] & 1, it.t0 + i))) break;
-            ++pcnt[w];
-            const bool fresh = s < 2;  // the group's first product of the item
-            if (fresh) {
-              if (used[w] && !(ok = wait_bar(sy, G::B_OEMPTY + w, (used[w] - 1) & 1, it.t0 + i))) break;
-              ++used[w];
-            }
-            tc_fence_after();
-            const uint64_t dv = dv0 + (uint64_t)(sl * (G::TILE >> 4));
+            for (int i = 0; i < it.n && ok; ++i) {
+              const uint32_t vs = (seq + 2 * i + 1) % G::NS, ks = (seq + 2 * i + 2) % G::NS;
+              if (!(ok = values(i))) break;
+              for (int w = 0; w < 2 && ok; ++w) {
+                if (!(ok = wait_on(sy, G::B_PFULL + w, pcnt[w] & 1, it.t0 + i))) break;
+                ++pcnt[w];
+                if (i == 0 && !(ok = o_free(w))) break;
+                tc_fence_after();
+                const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_bf16_ts(tbase + G::T_O + w * D, tbase + G::T_S + w * kTile + kk * 8, dv + ((kk * 2048) >> 4), ID_PV,
-                           (!fresh || kk > 0) ? 1u : 0u);
-            if (!two || w == 1) umma_commit(bars + G::B_EMPTY + sl);
-            if (s >= ns - 2) umma_commit(bars + G::B_OFULL + w);  // the group's last product
-            if (s + 2 < ns) ok = qk(s + 2);
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  umma_bf16_ts(tbase + G::T_O + w * D, tbase + G::T_S + w * kTile + kk * 8, dv + ((kk * 2048) >> 4),
+                               ID_PV, (i > 0 || kk > 0) ? 1u : 0u);
+                if (w == 1) umma_commit(bars + G::B_EMPTY + vs);
+                if (i + 1 == it.n) {
+                  umma_commit(bars + G::B_OFULL + w);
+                } else {
+                  if (w == 0 && !(ok = keys(i + 1))) break;
+                  qk(w, w, ks);
+                  if (w == 1) {
+                    umma_commit(bars + G::B_EMPTY + ks);
+                    if (i + 2 == it.n) umma_commit(bars + G::B_QEMPTY);
+                  }
+                }
+              }
+            }
+          } else {
+            // QK(0) QK(1), then for each tile: PV of the two groups' halves of its keys, QK two tiles ahead
+            auto step = [&](int i) -> bool {
+              if (!keys(i)) return false;
+              const uint32_t ks = (seq + 2 * i) % G::NS;
+              qk(i & 1, 0, ks);
+              umma_commit(bars + G::B_EMPTY + ks);
+              if (i + 1 == it.n) umma_commit(bars + G::B_QEMPTY);
+              return true;
+            };
+            ok = ok && step(0) && (it.n < 2 || step(1));
+            for (int i = 0; i < it.n && ok; ++i) {
+              const int b = i & 1;
+              const uint32_t vs = (seq + 2 * i + 1) % G::NS;
+              if (!(ok = values(i))) break;
+              if (i == 0 && !(ok = o_free(0) && o_free(1))) break;
+              if (!(ok = wait_on(sy, G::B_PSPLIT + b, bcnt[b] & 1, it.t0 + i))) break;
+              ++bcnt[b];
+              tc_fence_after();
+              const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_ts(tbase + G::T_O + (kk >> 2) * D, tbase + G::T_S + b * kTile + (kk >> 2) * 64 + (kk & 3) * 8,
+                             dv + ((kk * 2048) >> 4), ID_PV, (i > 0 || (kk & 3) > 0) ? 1u : 0u);
+              umma_commit(bars + G::B_ODONE);
+              umma_commit(bars + G::B_EMPTY + vs);
+              if (i + 1 == it.n) {
+                umma_commit(bars + G::B_OFULL);
+                umma_commit(bars + G::B_OFULL + 1);
+              }
+              if (i + 2 < it.n) ok = step(i + 2);
+            }
           }
           seq += 2 * it.n;
         }
@@ -550,11 +685,11 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       bool ok = true;
       const int t = tid - 64;
       while (ok && walk.next(a, it)) {
-        if (lane == 0) bad[(items & 15) * 4 + warp - 2] = 0;
+        if (lane == 0) bad[(items & 15) * 16 + warp - 2] = 0;
         __syncwarp();
         for (int i = 0; i < 2 * it.n; ++i, ++seq) {
           const uint32_t sl = seq % G::NS;
-          if (!(ok = wait_bar_warp(sy, G::B_FULL + sl, (seq / G::NS) & 1, it.t0 + (i >> 1)))) break;
+          if (!(ok = wait_on_warp(sy, G::B_FULL + sl, (seq / G::NS) & 1, it.t0 + (i >> 1)))) break;
           Reach r;
           if ((i & 1) && partly(r = reach(a, it.e, it.t0 + (i >> 1)))) {
             uint8_t *v = op_slot(sl);
@@ -575,7 +710,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                 }
               }
             }
-            if (found) bad[(items & 15) * 4 + warp - 2] = 1;
+            if (found) bad[(items & 15) * 16 + warp - 2] = 1;
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -590,112 +725,267 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   } else if (warp < 12) {
     reg_alloc<G::R_SOFT>();
     // ---------------------------------------------------------------- softmax groups
-    const int w = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int w = (warp - 4) >> 2, quad = warp & 3;
+    // rows lie in tensor memory lanes 32 q + l: 32 a quarter, or with 64-row tiles 16 (l < 16)
+    const int r = quad * G::WROWS + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t ts_addr = tbase + G::T_S + w * kTile + lane_off;
+    const uint32_t ts_addr = tbase + G::T_S + lane_off;
     const uint32_t to_addr = tbase + G::T_O + lane_off;
     const float c = a.c, thr = 8.f / c;
-    uint32_t scnt = 0, ocnt[2] = {0, 0}, mcnt = 0, items = 0;
+    uint32_t scnt[2] = {0, 0}, ocnt[2] = {0, 0}, mcnt = 0, dcnt = 0, items = 0;
     bool ok = true;
     while (ok && walk.next(a, it)) {
-      const bool two = it.e.ntok > a.tpt;
+      const bool two = NQ == 2 && it.e.ntok > a.tpt;
       const int tk = (two ? w * a.tpt : 0) + r / a.g;
-      const bool valid = r < a.g * a.tpt && tk < it.e.ntok;
+      const bool valid = lane < G::WROWS && r < a.g * a.tpt && tk < it.e.ntok;
       const bool active = __any_sync(0xffffffffu, valid);
-      int64_t lo, hi;
+      // Warps without a row take no part in the tiles: rows fill them in order, the first arrives for them too.
+      const int rows = min(a.g * a.tpt, max(0, (it.e.ntok - (two ? w * a.tpt : 0)) * a.g));
+      const int idle = 4 - max(1, (rows + G::WROWS - 1) / G::WROWS);
+      const bool part_of = active || quad == 0;
+      int lo, hi;
       sees(a, it.e, tk, lo, hi);
       if (!valid) lo = hi = 0;
       float m = -INFINITY, l = 0.f;
-      for (int i = two ? 0 : w; i < it.n; i += two ? 1 : 2) {
-        if (!(ok = wait_bar_warp(sy, G::B_SFULL + w, scnt & 1, it.t0 + i))) break;
-        ++scnt;
-        if (active) {
-          tc_fence_after();
-          uint32_t s[4][32];
+      if (two) {
+        // ---- this group's query tile: a lane is a row
+        const uint32_t sw = ts_addr + w * kTile, ow = to_addr + w * D;
+        for (int i = 0; i < it.n && part_of; ++i) {
+          if (!(ok = wait_on_warp(sy, G::B_SFULL + w, (scnt[w] + i) & 1, it.t0 + i))) break;
+          if (active) {
+            tc_fence_after();
+              // Two passes over S, 64 columns at a time (a second read of tensor memory costs less than the registers
+              // and the straight-line code of holding 128 columns): the row's maximum, then the weights.  P's columns
+              // [32 h, 32 h + 32) lie over S's, which are read by then.
+              const int va = in_tile(lo, (it.t0 + i) * kTile), vb = in_tile(hi, (it.t0 + i) * kTile);
+              const uint32_t width = (uint32_t)max(vb - va, 0);
+              const bool masked = __any_sync(0xffffffffu, va > 0 || vb < kTile);
+              uint32_t s[2][32];
+              auto load_half = [&](int hf) {
+                tmem_ld_32x32b_x32(sw + 64 * hf, s[0]);
+                tmem_ld_32x32b_x32(sw + 64 * hf + 32, s[1]);
+                tmem_wait_ld();
+                if (masked) {
+                  const int base = 64 * hf - va;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts_addr + 32 * q, s[q]);
-          tmem_wait_ld();
-          const int64_t ts = (int64_t)(it.t0 + i) * kTile;
-          const int va = (int)min(max(lo - ts, (int64_t)0), (int64_t)kTile);
-          const int vb = (int)min(max(hi - ts, (int64_t)0), (int64_t)kTile);
-          if (__any_sync(0xffffffffu, va > 0 || vb < kTile)) {
-            const uint32_t width = (uint32_t)max(vb - va, 0);
+                  for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if ((uint32_t)(32 * q + j - va) >= width) s[q][j] = 0xFF800000u;
-          }
-          float mx4[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            mx4[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-            for (int j = 1; j < 32; ++j) mx4[q] = fmaxf(mx4[q], __uint_as_float(s[q][j]));
-          }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          if (m == -INFINITY) m = mx;  // nothing summed yet: O's row is not there, or zero
-          const bool up = mx > m + thr;
-          if (__any_sync(0xffffffffu, up)) {
-            const float f = up ? ex2((m - mx) * c) : 1.f;
-            if (up) m = mx;
-            l *= f;
+                    for (int j = 0; j < 32; ++j)
+                      if ((uint32_t)(base + 32 * q + j) >= width) s[q][j] = 0xFF800000u;
+                }
+              };
+              float mx = -INFINITY;
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to_addr + w * D + 32 * q, o);
-              tmem_wait_ld();
+              for (int hf = 0; hf < 2; ++hf) {
+                load_half(hf);
+                float m4[4];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_32x32b_x32(to_addr + w * D + 32 * q, o);
-            }
+                for (int x = 0; x < 4; ++x) {
+                  m4[x] = __uint_as_float(s[x >> 1][16 * (x & 1)]);
+#pragma unroll
+                  for (int j = 1; j < 16; ++j) m4[x] = fmaxf(m4[x], __uint_as_float(s[x >> 1][16 * (x & 1) + j]));
+                }
+                mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+              }
+              if (m == -INFINITY) m = mx;  // nothing summed yet: O's row is not there, or zero
+              const bool up = mx > m + thr;
+              if (__any_sync(0xffffffffu, up)) {
+                const float f = up ? ex2((m - mx) * c) : 1.f;
+                if (up) m = mx;
+                l *= f;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t o[32];
+                  tmem_ld_32x32b_x32(ow + 32 * q, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                  tmem_st_32x32b_x32(ow + 32 * q, o);
+                }
+              }
+              const float mc = m == -INFINITY ? 0.f : m * c;
+              float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+              for (int hf = 0; hf < 2; ++hf) {
+                load_half(hf);
+                uint32_t p[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const int q = j >> 4, k = 2 * (j & 15);
+                  const float x = ex2(fmaf(__uint_as_float(s[q][k]), c, -mc));
+                  const float y = ex2(fmaf(__uint_as_float(s[q][k + 1]), c, -mc));
+                  l4[j & 1] += x;
+                  l4[2 + (j & 1)] += y;
+                  p[j] = pack2(x, y);
+                }
+                tmem_st_32x32b_x32(sw + 32 * hf, p);
+              }
+              l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            tmem_wait_st();
+            tc_fence_before();
           }
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t p[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int q = 2 * hf + (j >> 4), k = 2 * (j & 15);
-              const float x = ex2(fmaf(__uint_as_float(s[q][k]), c, -mc));
-              const float y = ex2(fmaf(__uint_as_float(s[q][k + 1]), c, -mc));
-              l4[j & 1] += x;
-              l4[2 + (j & 1)] += y;
-              p[j] = pack2(x, y);
-            }
-            tmem_st_32x32b_x32(ts_addr + 32 * hf, p);
-          }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          tmem_wait_st();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_n(bars + G::B_PFULL + w, quad == 0 ? 1 + idle : 1);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + G::B_PFULL + w);
+        scnt[0] += it.n;
+        scnt[1] += it.n;
+      } else {
+        // ---- one query tile: this group's 64 keys of each tile.  The warp's 32 rows are two halves of 16 in the
+        // layout of 16 x 256-bit accesses: four lanes share a row, a lane has rows l / 4 and l / 4 + 8 of a half and
+        // 16 of its 64 columns.  (With 16 rows or fewer, as single tokens have, one half is taken and all lanes
+        // work.)  l is a lane's own sum until the end.
+        constexpr int XH = G::WROWS / 16;
+        float hm[XH][2], hl[XH][2];
+        int rlo[XH][2], rhi[XH][2];
+        bool act[XH];
+#pragma unroll
+        for (int x = 0; x < XH; ++x) {
+          act[x] = __any_sync(0xffffffffu, valid && (lane >> 4) == x);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            hm[x][y] = -INFINITY;
+            hl[x][y] = 0.f;
+            rlo[x][y] = __shfl_sync(0xffffffffu, lo, 16 * x + 8 * y + (lane >> 2)) - 64 * w;
+            rhi[x][y] = __shfl_sync(0xffffffffu, hi, 16 * x + 8 * y + (lane >> 2)) - 64 * w;
+          }
+        }
+        if (!part_of) {
+          scnt[0] += (it.n + 1) >> 1;
+          scnt[1] += it.n >> 1;
+          dcnt += it.n;
+        }
+        for (int i = 0; i < it.n && part_of; ++i, ++dcnt) {
+          const int b = i & 1;
+          if (!(ok = wait_on_warp(sy, G::B_SFULL + b, scnt[b] & 1, it.t0 + i))) break;
+          ++scnt[b];
+          if (active) {
+            tc_fence_after();
+            const int ts = (it.t0 + i) * kTile;
+#pragma unroll
+            for (int x = 0; x < XH; ++x) {
+              if (!act[x]) continue;
+              uint32_t s[32];
+              const uint32_t at = ts_addr + b * kTile + 64 * w + ((uint32_t)(16 * x) << 16);
+              tmem_ld_16x256b_x8(at, s);
+              int va[2], vb[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                va[y] = min(max(rlo[x][y] - ts, 0), 64);
+                vb[y] = min(max(rhi[x][y] - ts, 0), 64);
+              }
+              const bool part = va[0] > 0 || va[1] > 0 || vb[0] < 64 || vb[1] < 64;
+              tmem_wait_ld();
+              if (__any_sync(0xffffffffu, part)) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int base = 2 * (lane & 3) - va[y];
+                  const uint32_t width = (uint32_t)max(vb[y] - va[y], 0);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    if ((uint32_t)(base + 8 * (k >> 1) + (k & 1)) >= width) s[4 * (k >> 1) + 2 * y + (k & 1)] = 0xFF800000u;
+                }
+              }
+              float mx[2], f[2];
+              bool up = false;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float e0 = __uint_as_float(s[2 * y]), e1 = __uint_as_float(s[2 * y + 1]);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                  e0 = fmaxf(e0, __uint_as_float(s[4 * k + 2 * y]));
+                  e1 = fmaxf(e1, __uint_as_float(s[4 * k + 2 * y + 1]));
+                }
+                mx[y] = fmaxf(e0, e1);
+              }
+#pragma unroll
+              for (int o = 1; o < 4; o <<= 1) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, mx[0], o), y1 = __shfl_xor_sync(0xffffffffu, mx[1], o);
+                mx[0] = fmaxf(mx[0], y0);
+                mx[1] = fmaxf(mx[1], y1);
+              }
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                if (hm[x][y] == -INFINITY) hm[x][y] = mx[y];  // nothing summed yet: O's row is not there, or zero
+                const bool u = mx[y] > hm[x][y] + thr;
+                f[y] = u ? ex2((hm[x][y] - mx[y]) * c) : 1.f;
+                if (u) hm[x][y] = mx[y];
+                up = up || u;
+              }
+              if (__any_sync(0xffffffffu, up)) {  // O must hold the tile before
+                if (!wait_on_warp(sy, G::B_ODONE, (dcnt - 1) & 1, it.t0 + i)) ok = false;
+                tc_fence_after();
+                hl[x][0] *= f[0];
+                hl[x][1] *= f[1];
+#pragma unroll 1
+                for (int q = 0; q < D / 64; ++q) {
+                  uint32_t o[32];
+                  const uint32_t oa = to_addr + ((uint32_t)(16 * x) << 16) + w * D + 64 * q;
+                  tmem_ld_16x256b_x8(oa, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                  tmem_st_16x256b_x8(oa, o);
+                }
+              }
+              uint32_t p[16];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float mc = hm[x][y] == -INFINITY ? 0.f : hm[x][y] * c;
+                float la = 0.f, lb = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float x0 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * y]), c, -mc));
+                  const float x1 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * y + 1]), c, -mc));
+                  la += x0;
+                  lb += x1;
+                  p[2 * k + y] = pack2(x0, x1);
+                }
+                hl[x][y] += la + lb;
+              }
+              tmem_st_16x128b_x8(at, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) arrive_n(bars + G::B_PSPLIT + b, quad == 0 ? 1 + idle : 1);
+          if (!ok) break;
+        }
+        // statistics of row `lane`
+#pragma unroll
+        for (int x = 0; x < 2 * XH; ++x) {
+          float v = hl[x >> 1][x & 1];
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          v = __shfl_sync(0xffffffffu, v, (lane & 7) * 4);
+          const float u = __shfl_sync(0xffffffffu, hm[x >> 1][x & 1], (lane & 7) * 4);
+          if ((lane >> 3) == x) m = u, l = v;
+        }
       }
       if (!ok) break;
       // ------------------------------------------------------------------ epilogue
       const float mc = m * c;
       const bool mine = two || w == 0;
-      const int n1 = two ? it.n : it.n / 2;          // steps of group 1
-      if (!mine) {
-        if (n1 > 0) {  // O[1] complete: the previous item's statistics have been read
-          if (!(ok = wait_bar_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
-          ++ocnt[1];
-          ml[r] = make_float2(mc, l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + G::B_MERGE);
-        }
+      if (!mine) {  // O[1] complete: the previous item's statistics have been read
+        if (!(ok = part_of ? wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0)
+                           : wait_on_warp<true>(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0)))
+          break;
+        ++ocnt[1];
+        if (lane < G::WROWS) ml[r] = make_float2(mc, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + G::B_MERGE);
         ++items;
         continue;
       }
-      const bool join = !two && n1 > 0;
-      if (!(ok = wait_bar_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0))) break;
+      const bool join = !two;
+      if (!(ok = part_of ? wait_on_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0)
+                         : wait_on_warp<true>(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0)))
+        break;
       ++ocnt[w];
       float M = mc, L = l, w0 = 1.f, w1 = 0.f;
       if (join) {
-        if (!(ok = wait_bar_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
-        if (!(ok = wait_bar_warp(sy, G::B_MERGE, mcnt & 1, it.t0))) break;
+        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
+        if (!(ok = wait_on_warp(sy, G::B_MERGE, mcnt & 1, it.t0))) break;
         ++mcnt;
         const float2 o = ml[r];
         M = fmaxf(mc, o.x);
@@ -704,12 +994,12 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         w1 = ex2(o.x - base);
         L = w0 * l + w1 * o.y;
       }
-      if (w == 0 && n1 > 0) ++ocnt[1];  // group 0 follows group 1's phases
+      if (w == 0) ++ocnt[1];  // group 0 follows group 1's phases
       tc_fence_after();
       const bool whole = it.first && it.last;
       int any_bad = 0;
 #pragma unroll
-      for (int x = 0; x < (G::Q8 ? 4 : 2); ++x) any_bad |= bad[(items & 15) * 4 + x];
+      for (int x = 0; x < (G::Q8 ? G::CONV : 2); ++x) any_bad |= bad[(items & 15) * 16 + x];
       const int64_t tok = it.e.tok + tk;
       const int head = it.head * a.g + r % a.g;
       const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -794,7 +1084,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         if (before == (uint32_t)(c1 - c0)) {
           __threadfence();
           for (int rr = 0; rr < 32; ++rr) {
-            const int row = quad * 32 + rr;
+            const int row = quad * G::WROWS + rr;
             if (!__shfl_sync(0xffffffffu, (int)valid, rr)) continue;
             auto part = [&](int cc) -> int64_t { return ((2 * (int64_t)cc + (cc == c0 ? 1 : 0)) * 2 + tile) * kTile + row; };
             float mm = -INFINITY;
@@ -831,57 +1121,79 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   } else if (G::Q8) {
     reg_dealloc<G::R_CONV>();
     // ---------------------------------------------------------------- conversion
-    const int t = tid - 384;
     constexpr int NRr = G::NR > 0 ? G::NR : 1;
-    // D = 128 (codes under the 128-byte swizzle): eight lanes take half a row of rows a and a ^ 5 of an 8-row
-    // group, which spreads both their 16-byte reads and their 16-byte writes over all banks.  D = 64 (plain rows of
-    // 64 bytes): eight lanes take two rows.
-    const int q4 = t & 3, slab = D == 128 ? (t >> 3) & 1 : 0;
-    const int pair = (t >> 2) & 1;
-    const int r8 = D == 128 ? (pair ? ((t >> 4) & 3) ^ 5 : (t >> 4) & 3) : ((t >> 3) & 3) * 2 + pair;
-    constexpr int GROUPS = D == 128 ? 2 : 4;  // 8-row groups the 128 threads cover at once
-    const int grp = D == 128 ? t >> 6 : t >> 5;
-    uint32_t seq = 0, items = 0;
+    // Work is cut into passes of 16 codes a lane.  D = 128 (codes under the 128-byte swizzle): two pairs of rows a,
+    // a ^ 5 of an 8-row group; eight lanes take half a row of each of a pair, which spreads both their 16-byte reads
+    // and their 16-byte writes over all banks; the group's other four rows are a ^ 2.  D = 64 (plain rows of 64
+    // bytes): the 8 rows of a group.
+    // Every other four warps take the keys, the others the values: a set's waits and fences pass while the other works.
+    constexpr int PASSES = D == 128 ? 32 : 16, SET = G::Q8 ? G::CONV / 2 : 8, W0 = SET / 4;
+    const int q4 = lane & 3, slab = D == 128 ? (lane >> 3) & 1 : 0, cw = warp - 12;
+    const int kvi = (cw >> 2) & 1, ci = (cw & 3) + 4 * (cw >> 3);
+    const int r8 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    const int soff = r8 * D + (D == 128 ? ((slab * 4 + q4) ^ r8) : q4) * 16;
+    const int doff = slab * G::SLAB + r8 * 128 + ((2 * q4) ^ r8) * 16;  // the second 16 bytes: at ^ 16
+    int rs = kvi, os = kvi;
+    uint32_t rph = 0, oph = 1, items = 0;
     bool ok = true;
     while (ok && walk.next(a, it)) {
-      if (lane == 0) bad[(items & 15) * 4 + warp - 12] = 0;
+      if (lane == 0) bad[(items & 15) * 16 + cw] = 0;
       __syncwarp();
+      // Even shares beside two full softmax groups.  When the rows are few all of the softmax runs on the first quarter
+      // of the SM (the first rows belong to its warps): the conversion warps there take a sixteenth together.
+      const bool even = D == 64 || it.e.ntok * a.g > G::WROWS;
+      constexpr int P0 = PASSES / 16 / W0, P1 = (PASSES - W0 * P0) / (SET - W0);
+      const int few = (ci & 3) == 0 ? (ci >> 2) * P0 : W0 * P0 + (ci - 1 - (ci >> 2)) * P1;
+      const int first = even ? ci * (PASSES / SET) : few;
+      const int last = first + (even ? PASSES / SET : (ci & 3) == 0 ? P0 : P1);
       for (int i = 0; i < it.n && ok; ++i) {
         const Reach rc = reach(a, it.e, it.t0 + i);
-        for (int kvi = 0; kvi < 2; ++kvi, ++seq) {
-          const int rs = seq % NRr, os = seq % G::NS;
-          if (!(ok = wait_bar_warp(sy, G::B_RFULL + rs, (seq / NRr) & 1, it.t0 + i))) break;
-          if (!(ok = wait_bar_warp(sy, G::B_EMPTY + os, ((seq / G::NS) & 1) ^ 1, it.t0 + i))) break;
+        const bool part = partly(rc);
+        {
+          if (!(ok = wait_on_warp(sy, G::B_RFULL + rs, rph, it.t0 + i))) break;
+          // pass u: rows of group u / 2, the upper or lower four (D = 128), or of group u
           const uint8_t *src = raw_stage(rs);
-          uint8_t *dst = op_slot(os) + slab * G::SLAB;
+          const float *ss = sc + rs * kTile;
+          auto codes_at = [&](int u) {
+            return *reinterpret_cast<const uint4 *>(src + (D == 128 ? (u >> 1) * 1024 + (soff ^ ((u & 1) * 0x120)) : u * 512 + soff));
+          };
+          auto row_of = [&](int u) { return D == 128 ? (u >> 1) * 8 + (r8 ^ ((u & 1) * 2)) : u * 8 + r8; };
+          uint4 nw = codes_at(first);
+          float nf = ss[row_of(first)];
+          if (!(ok = wait_on_warp(sy, G::B_EMPTY + os, oph, it.t0 + i))) break;
+          uint8_t *dst = op_slot(os);
           int found = 0;
-#pragma unroll
-          for (int k = 0; k < 16 / GROUPS; ++k) {
-            const int row = (k * GROUPS + grp) * 8 + r8;
-            float s = sc[rs * kTile + row];
-            if (row < rc.a || row >= rc.d) s = 0.f;  // seen by none (codes are finite by construction)
-            if (kvi && !finite_f(s) && (row < rc.b || row >= rc.c)) {
-              s = 0.f;
-              found = 1;
+#pragma unroll 1
+          for (int u = first; u < last; ++u) {
+            const uint4 w = nw;
+            float f = nf;
+            const int row = row_of(u);
+            if (u + 1 < last) {  // ahead of this pass's stores
+              nw = codes_at(u + 1);
+              nf = ss[row_of(u + 1)];
             }
-            const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
-            const int cc = D == 128 ? ((slab * 4 + q4) ^ r8) : q4;
-            const uint4 u = *reinterpret_cast<const uint4 *>(src + row * D + cc * 16);
+            if (part) {
+              if (row < rc.a || row >= rc.d) f = 0.f;  // seen by none (codes are finite by construction)
+              if (kvi && !finite_f(f) && (row < rc.b || row >= rc.c)) {
+                f = 0.f;
+                found = 1;
+              }
+            }
             uint4 o0, o1;
-            o0.x = codes2<FMT>(u.x, 0, s2), o0.y = codes2<FMT>(u.x, 1, s2);
-            o0.z = codes2<FMT>(u.y, 0, s2), o0.w = codes2<FMT>(u.y, 1, s2);
-            o1.x = codes2<FMT>(u.z, 0, s2), o1.y = codes2<FMT>(u.z, 1, s2);
-            o1.z = codes2<FMT>(u.w, 0, s2), o1.w = codes2<FMT>(u.w, 1, s2);
-            *reinterpret_cast<uint4 *>(dst + row * 128 + (((2 * q4) ^ r8) << 4)) = o0;
-            *reinterpret_cast<uint4 *>(dst + row * 128 + (((2 * q4 + 1) ^ r8) << 4)) = o1;
+            convert16<FMT>(w, f, o0, o1);
+            const int at = D == 128 ? (u >> 1) * 1024 + (doff ^ ((u & 1) * 0x120)) : u * 1024 + doff;
+            *reinterpret_cast<uint4 *>(dst + at) = o0;
+            *reinterpret_cast<uint4 *>(dst + (at ^ 16)) = o1;
           }
-          if (found) bad[(items & 15) * 4 + warp - 12] = 1;
+          if (found) bad[(items & 15) * 16 + cw] = 1;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bars + G::B_FULL + os);
             mbar_arrive(bars + G::B_REMPTY + rs);
           }
+          if ((rs += 2) >= NRr) rs = kvi, rph ^= 1;
+          if ((os += 2) >= G::NS) os = kvi, oph ^= 1;
         }
       }
       ++items;
@@ -897,7 +1209,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
 }
 
 // ------------------------------------------------------------------ host side
-int tokens_per_tile(int g) { return kTile / g; }
+int tokens_per_tile(int g, int tiles) { return (tiles == 1 ? 64 : kTile) / g; }
 
 int box_rows(int64_t page_size) {  // largest power of two that divides the page, up to a tile
   int b = 1;
@@ -905,8 +1217,17 @@ int box_rows(int64_t page_size) {  // largest power of two that divides the page
   return b;
 }
 
+// Query tiles of an entry: one of 64 rows where the sequences have no more rows each on average (single tokens, drafts:
+// the two softmax groups take half of each key tile, and shared memory goes to more of those), else two of 128 (they
+// share the keys).
+int query_tiles(int64_t B, int64_t T, int64_t n_seqs, bool packed, int g) {
+  const int64_t tokens = packed ? T : B * T;
+  return g <= 64 && tokens <= n_seqs * tokens_per_tile(g, 1) ? 1 : 2;
+}
+
 int64_t max_entries(int64_t B, int64_t T, int64_t n_seqs, bool packed, int g) {
-  const int64_t per = 2 * tokens_per_tile(g);
+  const int tiles = query_tiles(B, T, n_seqs, packed, g);
+  const int64_t per = (int64_t)tiles * tokens_per_tile(g, tiles);
   return packed ? T / per + n_seqs : B * ((T + per - 1) / per);
 }
 
@@ -934,17 +1255,25 @@ Plan plan(int64_t e_max, int64_t n_seqs, int D, int G) {
   return p;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NQ>
 cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const PaArgs &a,
                        cudaStream_t stream) {
-  using G = PaCfg<D, FMT>;
-  auto kern = pa_kernel<D, FMT>;
+  using G = PaCfg<D, FMT, NQ>;
+  auto kern = pa_kernel<D, FMT, NQ>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   pa_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   kern<<<a.G, G::THREADS, G::SMEM_BYTES, stream>>>(mq, mk, mv, a);
   return cudaGetLastError();
+}
+
+template <int D, int NQ>
+cudaError_t launch_format(int format, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                          const PaArgs &a, cudaStream_t stream) {
+  if (format == LA_KV_E4M3) return launch_one<D, LA_KV_E4M3, NQ>(mq, mk, mv, a, stream);
+  if (format == LA_KV_INT8) return launch_one<D, LA_KV_INT8, NQ>(mq, mk, mv, a, stream);
+  return launch_one<D, LA_KV_BF16, NQ>(mq, mk, mv, a, stream);
 }
 
 }  // namespace
@@ -980,7 +1309,9 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int G, void *workspace, cudaStre
   p.page_size = a.c.page_size;
   p.box = box_rows(a.c.page_size);
   p.g = g;
-  p.tpt = tokens_per_tile(g);
+  const int tiles = query_tiles(a.B, a.T, a.n_seqs, a.cu_seqlens != nullptr, g);
+  p.tpt = tokens_per_tile(g, tiles);
+  p.per = p.tpt * tiles;
   p.Hkv = a.c.H;
   p.H = a.H;
   p.window = a.window;
@@ -1033,14 +1364,11 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int G, void *workspace, cudaStre
       return cudaErrorInvalidValue;
     }
   }
-  if (D == 64) {
-    if (a.c.format == LA_KV_E4M3) return launch_one<64, LA_KV_E4M3>(mq, mk, mv, p, stream);
-    if (a.c.format == LA_KV_INT8) return launch_one<64, LA_KV_INT8>(mq, mk, mv, p, stream);
-    return launch_one<64, LA_KV_BF16>(mq, mk, mv, p, stream);
-  }
-  if (a.c.format == LA_KV_E4M3) return launch_one<128, LA_KV_E4M3>(mq, mk, mv, p, stream);
-  if (a.c.format == LA_KV_INT8) return launch_one<128, LA_KV_INT8>(mq, mk, mv, p, stream);
-  return launch_one<128, LA_KV_BF16>(mq, mk, mv, p, stream);
+  if (tiles == 1)
+    return D == 64 ? launch_format<64, 1>(a.c.format, mq, mk, mv, p, stream)
+                   : launch_format<128, 1>(a.c.format, mq, mk, mv, p, stream);
+  return D == 64 ? launch_format<64, 2>(a.c.format, mq, mk, mv, p, stream)
+                 : launch_format<128, 2>(a.c.format, mq, mk, mv, p, stream);
 }
 
 cudaError_t pa_device_error(unsigned int *flags, unsigned int *where, bool reset) {
