@@ -316,6 +316,17 @@ struct PaCfg {
   static_assert(128 * R_AUX + 256 * R_SOFT + 32 * CONV * R_CONV <= THREADS * R_LAUNCH, "register split");
 };
 
+template <int V>
+struct Vec;
+template <>
+struct Vec<2> {
+  typedef float2 T;
+};
+template <>
+struct Vec<4> {
+  typedef float4 T;
+};
+
 // A piece of an entry: `n` key tiles from tile t0 on, of one cache head.
 struct Item {
   Entry e;
@@ -1083,36 +1094,56 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == (uint32_t)(c1 - c0)) {
           __threadfence();
-          for (int rr = 0; rr < 32; ++rr) {
-            const int row = quad * G::WROWS + rr;
-            if (!__shfl_sync(0xffffffffu, (int)valid, rr)) continue;
-            auto part = [&](int cc) -> int64_t { return ((2 * (int64_t)cc + (cc == c0 ? 1 : 0)) * 2 + tile) * kTile + row; };
-            float mm = -INFINITY;
-            for (int cc = c0 + lane; cc <= c1; cc += 32) mm = fmaxf(mm, __ldcg(&a.pml[part(cc)]).x);
+          // A lane keeps a row's statistics; eight rows at a time all lanes add up the parts, V columns each: as many
+          // loads are under way as registers hold.
+          constexpr int V = D / 32;
+          typedef typename Vec<V>::T VT;
+          const uint32_t rows_here = __ballot_sync(0xffffffffu, valid);
+          auto part_row = [&](int cc, int q) -> int64_t {
+            return ((2 * (int64_t)cc + (cc == c0 ? 1 : 0)) * 2 + tile) * kTile + quad * G::WROWS + q;
+          };
+          float mm = -INFINITY;
+#pragma unroll 8
+          for (int cc = c0; cc <= c1; ++cc) mm = fmaxf(mm, __ldcg(&a.pml[part_row(cc, lane)]).x);
+          const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 1
+          for (int r0 = 0; r0 < G::WROWS; r0 += 8) {
+            if (!((rows_here >> r0) & 0xFFu)) continue;
+            float acc[8][V], ls = 0.f;
 #pragma unroll
-            for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-            const float base = mm == -INFINITY ? 0.f : mm;
-            float acc[D / 32], ls = 0.f;
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) acc[u] = 0.f;
-#pragma unroll 4
+              for (int u = 0; u < V; ++u) acc[k][u] = 0.f;
+#pragma unroll 2
             for (int cc = c0; cc <= c1; ++cc) {
-              const float2 x = __ldcg(&a.pml[part(cc)]);
+              VT v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const VT *>(a.po + part_row(cc, r0 + k) * D) + lane);
+              const float2 x = __ldcg(&a.pml[part_row(cc, lane)]);
               const float wt = ex2(x.x - base);
               ls = fmaf(wt, x.y, ls);
-              const float *src = a.po + part(cc) * D + lane;
 #pragma unroll
-              for (int u = 0; u < D / 32; ++u) acc[u] = fmaf(wt, __ldcg(src + 32 * u), acc[u]);
+              for (int k = 0; k < 8; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, wt, r0 + k);
+#pragma unroll
+                for (int u = 0; u < V; ++u) acc[k][u] = fmaf(wk, reinterpret_cast<const float *>(&v[k])[u], acc[k][u]);
+              }
             }
             const float iv = ls == 0.f ? 0.f : 1.f / ls;
-            const int64_t rt = it.e.tok + (two ? w * a.tpt : 0) + row / a.g;
-            const int rh = it.head * a.g + row % a.g;
-            __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(a.out) + (int64_t)it.e.b * a.o_sb + rt * a.o_st +
-                                 (int64_t)rh * a.o_sh + lane;
+            const float row_lse = (mm + log2f(ls)) * 0.6931471805599453f;
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) dst[32 * u] = __float2bfloat16_rn(acc[u] * iv);
-            if (a.lse && lane == 0)
-              a.lse[((int64_t)it.e.b * a.T + rt) * a.H + rh] = (mm + log2f(ls)) * 0.6931471805599453f;
+            for (int k = 0; k < 8; ++k) {
+              const float ik = __shfl_sync(0xffffffffu, iv, r0 + k);
+              const int row = quad * G::WROWS + r0 + k;
+              const int64_t rt = it.e.tok + (two ? w * a.tpt : 0) + row / a.g;
+              const int rh = it.head * a.g + row % a.g;
+              if (!((rows_here >> (r0 + k)) & 1u)) continue;
+              uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + (int64_t)it.e.b * a.o_sb +
+                                                           rt * a.o_st + (int64_t)rh * a.o_sh + V * lane);
+#pragma unroll
+              for (int u = 0; u < V / 2; ++u) dst[u] = pack2(acc[k][2 * u] * ik, acc[k][2 * u + 1] * ik);
+              if (a.lse && lane == r0 + k) a.lse[((int64_t)it.e.b * a.T + rt) * a.H + rh] = row_lse;
+            }
           }
         }
       }
