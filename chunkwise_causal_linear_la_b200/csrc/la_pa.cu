@@ -296,7 +296,8 @@ struct PaCfg {
                        B_QEMPTY = B_QFULL + 1, B_SFULL = B_QFULL + 2, B_PFULL = B_QFULL + 4, B_OFULL = B_QFULL + 6,
                        B_OEMPTY = B_QFULL + 8, B_MERGE = B_QFULL + 10, B_DRAIN = B_QFULL + 11,
                        B_PSPLIT = B_QFULL + 12, B_ODONE = B_QFULL + 14,  // one query tile: P of both groups; PV done
-                       B_READY = B_QFULL + 15,  // bf16, per slot: fixed up
+                       B_PHALF = B_QFULL + 15,  // two query tiles: P's second half (PFULL: the first)
+                       B_READY = B_QFULL + 17,  // bf16, per slot: fixed up
                        NBAR = B_READY + (Q8 ? 0 : NS);
   // per item (mod 16) and fix-up or conversion warp: values that are not finite were taken out.  (A flag left
   // from 16 items before only costs a look for such values.)
@@ -471,6 +472,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       if (i >= G::B_OEMPTY && i < G::B_OEMPTY + 2) cnt = 4;
       if (i == G::B_MERGE) cnt = 4;
       if (i >= G::B_PSPLIT && i < G::B_PSPLIT + 2) cnt = 8;
+      if (i >= G::B_PHALF && i < G::B_PHALF + 2) cnt = 4;
       if (i >= G::B_READY) cnt = 2;  // fix-up warps
       mbar_init(bars + i, cnt);
     }
@@ -576,117 +578,132 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         __syncwarp();
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        // ---------------------------------------------------------- MMA issuer
-          constexpr uint32_t ID_QK = idesc_bf16_f32(G::ROWS, kTile, 0, 0);
-        constexpr uint32_t ID_PV = idesc_bf16_f32(G::ROWS, D, 0, 1);
-        const uint64_t dq0 = smem_desc_sw128(smem_u32(sm + G::OFF_Q), 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(smem_u32(op_slot(0)), 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(smem_u32(op_slot(0)), G::SLAB, 1024);
-        uint32_t seq = 0, items = 0, used[2] = {0, 0}, pcnt[2] = {0, 0}, bcnt[2] = {0, 0};
-        bool ok = true;
-        // S[w] = Q[qt] K^T for the keys in slot sl
-        auto qk = [&](int w, int qt, uint32_t sl) {
-          tc_fence_after();
-          const uint64_t dq = dq0 + (uint64_t)(qt * (G::QTILE >> 4));
-          const uint64_t dk = dk0 + (uint64_t)(sl * (G::TILE >> 4));
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp walks and waits, so that descriptors and addresses are uniform; one lane issues.
+        constexpr uint32_t ID_QK = idesc_bf16_f32(G::ROWS, kTile, 0, 0);
+      constexpr uint32_t ID_PV = idesc_bf16_f32(G::ROWS, D, 0, 1);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(sm + G::OFF_Q), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(op_slot(0)), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(op_slot(0)), G::SLAB, 1024);
+      uint32_t seq = 0, items = 0, used[2] = {0, 0}, pcnt[2] = {0, 0}, bcnt[2] = {0, 0};
+      bool ok = true;
+      // S[w] = Q[qt] K^T for the keys in slot sl
+      auto qk = [&](int w, int qt, uint32_t sl) {
+        tc_fence_after();
+        const uint64_t dq = dq0 + (uint64_t)(qt * (G::QTILE >> 4));
+        const uint64_t dk = dk0 + (uint64_t)(sl * (G::TILE >> 4));
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
+          for (int kk = 0; kk < D / 16; ++kk)
             umma_bf16(tbase + G::T_S + w * kTile, dq + (((kk >> 2) * G::QSLAB + (kk & 3) * 32) >> 4),
                       dk + (((kk >> 2) * G::SLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
-          }
           umma_commit(bars + G::B_SFULL + w);
-        };
-        auto keys = [&](int i) -> bool {  // tile i's keys are in their slot
-          const uint32_t k = seq + 2 * i;
-          return wait_on(sy, G::B_FULL + k % G::NS, (k / G::NS) & 1, it.t0 + i);
-        };
-        auto values = [&](int i) -> bool {
-          const uint32_t k = seq + 2 * i + 1;
-          const bool fix = !G::Q8 && partly(reach(a, it.e, it.t0 + i));
-          return wait_on(sy, (fix ? G::B_READY : G::B_FULL) + k % G::NS, (k / G::NS) & 1, it.t0 + i);
-        };
-        auto o_free = [&](int w) -> bool {  // O[w] of the item before has been read
-          if (used[w] && !wait_on(sy, G::B_OEMPTY + w, (used[w] - 1) & 1, it.t0)) return false;
-          ++used[w];
-          return true;
-        };
-        while (ok && walk.next(a, it)) {
-          const bool two = NQ == 2 && it.e.ntok > a.tpt;
-          ok = wait_on(sy, G::B_QFULL, items & 1, it.t0);
-          ++items;
-          if (two) {
-            // QK(0, K0) QK(1, K0), then for each tile and group w: PV(w, Vi), QK(w, Ki+1)
-            if (ok && (ok = keys(0))) {
-              qk(0, 0, seq % G::NS);
-              qk(1, 1, seq % G::NS);
-              umma_commit(bars + G::B_EMPTY + seq % G::NS);
-              if (it.n == 1) umma_commit(bars + G::B_QEMPTY);
-            }
-            for (int i = 0; i < it.n && ok; ++i) {
-              const uint32_t vs = (seq + 2 * i + 1) % G::NS, ks = (seq + 2 * i + 2) % G::NS;
-              if (!(ok = values(i))) break;
-              for (int w = 0; w < 2 && ok; ++w) {
-                if (!(ok = wait_on(sy, G::B_PFULL + w, pcnt[w] & 1, it.t0 + i))) break;
-                ++pcnt[w];
-                if (i == 0 && !(ok = o_free(w))) break;
+        }
+        __syncwarp();
+      };
+      auto commit = [&](int bar) {
+        if (elect_one()) umma_commit(bars + bar);
+        __syncwarp();
+      };
+      auto keys = [&](int i) -> bool {  // tile i's keys are in their slot
+        const uint32_t k = seq + 2 * i;
+        return wait_on_warp(sy, G::B_FULL + k % G::NS, (k / G::NS) & 1, it.t0 + i);
+      };
+      auto values = [&](int i) -> bool {
+        const uint32_t k = seq + 2 * i + 1;
+        const bool fix = !G::Q8 && partly(reach(a, it.e, it.t0 + i));
+        return wait_on_warp(sy, (fix ? G::B_READY : G::B_FULL) + k % G::NS, (k / G::NS) & 1, it.t0 + i);
+      };
+      auto o_free = [&](int w) -> bool {  // O[w] of the item before has been read
+        if (used[w] && !wait_on_warp(sy, G::B_OEMPTY + w, (used[w] - 1) & 1, it.t0)) return false;
+        ++used[w];
+        return true;
+      };
+      while (ok && walk.next(a, it)) {
+        const bool two = NQ == 2 && it.e.ntok > a.tpt;
+        ok = wait_on_warp(sy, G::B_QFULL, items & 1, it.t0);
+        ++items;
+        if (two) {
+          // QK(0, K0) QK(1, K0), then for each tile and group w: PV(w, Vi), QK(w, Ki+1)
+          if (ok && (ok = keys(0))) {
+            qk(0, 0, seq % G::NS);
+            qk(1, 1, seq % G::NS);
+            commit(G::B_EMPTY + seq % G::NS);
+            if (it.n == 1) commit(G::B_QEMPTY);
+          }
+          for (int i = 0; i < it.n && ok; ++i) {
+            const uint32_t vs = (seq + 2 * i + 1) % G::NS, ks = (seq + 2 * i + 2) % G::NS;
+            if (!(ok = values(i))) break;
+            for (int w = 0; w < 2 && ok; ++w) {
+              if (i == 0 && !(ok = o_free(w))) break;
+              const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
+              // the first half of P's keys is multiplied while the second is worked out
+              for (int hf = 0; hf < 2 && ok; ++hf) {
+                if (!(ok = wait_on_warp(sy, (hf ? G::B_PHALF : G::B_PFULL) + w, pcnt[w] & 1, it.t0 + i))) break;
                 tc_fence_after();
-                const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  umma_bf16_ts(tbase + G::T_O + w * D, tbase + G::T_S + w * kTile + kk * 8, dv + ((kk * 2048) >> 4),
-                               ID_PV, (i > 0 || kk > 0) ? 1u : 0u);
-                if (w == 1) umma_commit(bars + G::B_EMPTY + vs);
-                if (i + 1 == it.n) {
-                  umma_commit(bars + G::B_OFULL + w);
-                } else {
-                  if (w == 0 && !(ok = keys(i + 1))) break;
-                  qk(w, w, ks);
-                  if (w == 1) {
-                    umma_commit(bars + G::B_EMPTY + ks);
-                    if (i + 2 == it.n) umma_commit(bars + G::B_QEMPTY);
-                  }
+                  for (int kk = 0; kk < kTile / 32; ++kk)
+                    umma_bf16_ts(tbase + G::T_O + w * D, tbase + G::T_S + w * kTile + hf * 32 + kk * 8,
+                                 dv + (((hf * 4 + kk) * 2048) >> 4), ID_PV, (i > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+              }
+              if (!ok) break;
+              ++pcnt[w];
+              if (w == 1) commit(G::B_EMPTY + vs);
+              if (i + 1 == it.n) {
+                commit(G::B_OFULL + w);
+              } else {
+                if (w == 0 && !(ok = keys(i + 1))) break;
+                qk(w, w, ks);
+                if (w == 1) {
+                  commit(G::B_EMPTY + ks);
+                  if (i + 2 == it.n) commit(G::B_QEMPTY);
                 }
               }
             }
-          } else {
-            // QK(0) QK(1), then for each tile: PV of the two groups' halves of its keys, QK two tiles ahead
-            auto step = [&](int i) -> bool {
-              if (!keys(i)) return false;
-              const uint32_t ks = (seq + 2 * i) % G::NS;
-              qk(i & 1, 0, ks);
-              umma_commit(bars + G::B_EMPTY + ks);
-              if (i + 1 == it.n) umma_commit(bars + G::B_QEMPTY);
-              return true;
-            };
-            ok = ok && step(0) && (it.n < 2 || step(1));
-            for (int i = 0; i < it.n && ok; ++i) {
-              const int b = i & 1;
-              const uint32_t vs = (seq + 2 * i + 1) % G::NS;
-              if (!(ok = values(i))) break;
-              if (i == 0 && !(ok = o_free(0) && o_free(1))) break;
-              if (!(ok = wait_on(sy, G::B_PSPLIT + b, bcnt[b] & 1, it.t0 + i))) break;
-              ++bcnt[b];
-              tc_fence_after();
-              const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
+          }
+        } else {
+          // QK(0) QK(1), then for each tile: PV of the two groups' halves of its keys, QK two tiles ahead
+          auto step = [&](int i) -> bool {
+            if (!keys(i)) return false;
+            const uint32_t ks = (seq + 2 * i) % G::NS;
+            qk(i & 1, 0, ks);
+            commit(G::B_EMPTY + ks);
+            if (i + 1 == it.n) commit(G::B_QEMPTY);
+            return true;
+          };
+          ok = ok && step(0) && (it.n < 2 || step(1));
+          for (int i = 0; i < it.n && ok; ++i) {
+            const int b = i & 1;
+            const uint32_t vs = (seq + 2 * i + 1) % G::NS;
+            if (!(ok = values(i))) break;
+            if (i == 0 && !(ok = o_free(0) && o_free(1))) break;
+            if (!(ok = wait_on_warp(sy, G::B_PSPLIT + b, bcnt[b] & 1, it.t0 + i))) break;
+            ++bcnt[b];
+            tc_fence_after();
+            const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
                 umma_bf16_ts(tbase + G::T_O + (kk >> 2) * D, tbase + G::T_S + b * kTile + (kk >> 2) * 64 + (kk & 3) * 8,
                              dv + ((kk * 2048) >> 4), ID_PV, (i > 0 || (kk & 3) > 0) ? 1u : 0u);
-              umma_commit(bars + G::B_ODONE);
-              umma_commit(bars + G::B_EMPTY + vs);
-              if (i + 1 == it.n) {
-                umma_commit(bars + G::B_OFULL);
-                umma_commit(bars + G::B_OFULL + 1);
-              }
-              if (i + 2 < it.n) ok = step(i + 2);
             }
+            __syncwarp();
+            commit(G::B_ODONE);
+            commit(G::B_EMPTY + vs);
+            if (i + 1 == it.n) {
+              commit(G::B_OFULL);
+              commit(G::B_OFULL + 1);
+            }
+            if (i + 2 < it.n) ok = step(i + 2);
           }
-          seq += 2 * it.n;
         }
-        umma_commit(bars + G::B_DRAIN);  // products under way end before tensor memory is freed
-        drain_bar(sy, G::B_DRAIN, 0);
+        seq += 2 * it.n;
       }
+      commit(G::B_DRAIN);  // products under way end before tensor memory is freed
+      drain_bar(sy, G::B_DRAIN, 0);
       __syncwarp();
     } else if (!G::Q8) {
       // -------------------------------------------------------------- values fix-up
@@ -830,13 +847,17 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   p[j] = pack2(x, y);
                 }
                 tmem_st_32x32b_x32(sw + 32 * hf, p);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_n(bars + (hf ? G::B_PHALF : G::B_PFULL) + w, quad == 0 ? 1 + idle : 1);
               }
               l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            tmem_wait_st();
-            tc_fence_before();
+          } else if (lane == 0) {
+            arrive_n(bars + G::B_PFULL + w, 4);
+            arrive_n(bars + G::B_PHALF + w, 4);
           }
           __syncwarp();
-          if (lane == 0) arrive_n(bars + G::B_PFULL + w, quad == 0 ? 1 + idle : 1);
         }
         scnt[0] += it.n;
         scnt[1] += it.n;
