@@ -606,44 +606,66 @@ def kv_cache(n_pages, page_size, H, D, dtype=torch.bfloat16, device="cuda"):
 def describe_cache(k, v, k_scale=None, v_scale=None) -> LaKvCache:
     """la_kv_cache for [n_pages, page_size, H, D] pages of keys and values (D contiguous, the other
     axes in any order, the same strides for both) and their [n_pages, H, page_size] scales."""
-    if k.dim() != 4 or k.shape != v.shape:
+    shape = k.shape
+    if len(shape) != 4 or shape != v.shape:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, H, D] tensors of one shape")
-    if k.dtype not in _KV or v.dtype != k.dtype:
+    fmt = _KV.get(k.dtype)
+    if fmt is None or v.dtype != k.dtype:
         raise TypeError("k_cache and v_cache must share one dtype: bfloat16, float8_e4m3fn or int8")
-    n, p, H, D = k.shape
-    strides = [(k.stride(i), v.stride(i)) for i in range(3) if k.shape[i] > 1]
-    if (D > 1 and (k.stride(3) != 1 or v.stride(3) != 1)) or any(a != b for a, b in strides):
+    n, p, H, D = shape
+    ks, vs = k.stride(), v.stride()
+    if (D > 1 and (ks[3] != 1 or vs[3] != 1)) or (
+            ks != vs and any(ks[i] != vs[i] for i in range(3) if shape[i] > 1)):
         raise ValueError("k_cache and v_cache must have equal strides and a contiguous head dim")
-    eight = k.dtype != torch.bfloat16
+    if fmt == LA_KV_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise TypeError("a bfloat16 cache has no scales")
+        return LaKvCache(k.data_ptr(), v.data_ptr(), None, None, fmt, n, p, H, D, ks[0], ks[1], ks[2])
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if not eight and t is not None:
-            raise TypeError("%s: a bfloat16 cache has no scales" % name)
-        if eight and (t is None or t.dtype != torch.float32 or tuple(t.shape) != (n, H, p) or not t.is_contiguous()):
+        if t is None or t.dtype != torch.float32 or t.shape != (n, H, p) or not t.is_contiguous():
             raise TypeError("%s must be a contiguous float32 [n_pages, H, page_size] tensor" % name)
-    return LaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if eight else None,
-                     v_scale.data_ptr() if eight else None, _KV[k.dtype], n, p, H, D, k.stride(0), k.stride(1),
-                     k.stride(2))
+    return LaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), fmt, n, p, H, D, ks[0], ks[1],
+                     ks[2])
 
 
-def _on_current_device(**tensors):
-    """The calls launch on the current device, in its current stream: tensors of another one are refused."""
-    for name, t in tensors.items():
-        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
-            raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+def _device_of(*tensors) -> int:
+    """The current device.  The calls launch there, in its current stream: tensors of another one are refused."""
+    at = [t.get_device() for t in tensors if t is not None]
+    if min(at) < 0 or min(at) != max(at) or at[0] != torch._C._cuda_getDevice():
+        raise ValueError("tensors on devices %s: all have to be on the current CUDA device" % sorted(set(at)))
+    return at[0]
+
+
+def _stream_of(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+def _describe(t: torch.Tensor) -> LaTensor:
+    """describe(), in fewer steps: these calls are made once a layer and token."""
+    shape, st, dt = t.shape, t.stride(), _DT.get(t.dtype)
+    if len(shape) != 4 or dt is None or (shape[3] > 1 and st[3] != 1):
+        return describe(t)  # says what is wrong
+    return LaTensor(t.data_ptr(), dt, shape[0], shape[1], shape[2], shape[3], st[0], st[1], st[2])
+
+
+_SIZE_MAX = ctypes.c_size_t(-1).value
+_here = contextlib.nullcontext()
 
 
 def _allocating_for(stream):
     """Outputs and workspace made for a call on `stream` belong to that stream in torch's allocator, so
     that their memory is not handed to other work before the call has run."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _index(name, t, shape):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError("%s must be a contiguous int32 tensor of shape %s" % (name, list(shape)))
-    return None if t is None else t.data_ptr()
+    return t.data_ptr()
 
 
 def _n_seqs(B, cu_seqlens):
@@ -657,7 +679,7 @@ def _n_seqs(B, cu_seqlens):
 def _table(page_table, n):
     if page_table.dim() != 2 or page_table.shape[0] != n:
         raise TypeError("page_table must be [n_seqs, max_pages]")
-    return _index("page_table", page_table, tuple(page_table.shape)), page_table.shape[1]
+    return _index("page_table", page_table, page_table.shape), page_table.shape[1]
 
 
 def la_kv_write(k, v, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_scale=None, v_scale=None,
@@ -668,11 +690,9 @@ def la_kv_write(k, v, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_s
     lib = load_library()
     n = _n_seqs(k.shape[0], cu_seqlens)
     cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
-    tk, tv, tl, tc = describe(k), describe(v), _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
-    _on_current_device(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                       page_table=page_table, kv_len=kv_len, cu_seqlens=cu_seqlens)
-    st = lib.la_kv_write(ctypes.byref(tk), ctypes.byref(tv), tc, n, ctypes.byref(cache), table, max_pages, tl,
-                         _stream(stream))
+    tk, tv, tl, tc = _describe(k), _describe(v), _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
+    dev = _device_of(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_len, cu_seqlens)
+    st = lib.la_kv_write(tk, tv, tc, n, cache, table, max_pages, tl, _stream_of(stream, dev))
     _check(lib, st, "la_kv_write")
 
 
@@ -685,20 +705,16 @@ def la_kv_read(k_cache, v_cache, page_table, T, start=None, cu_seqlens=None, k_s
     n = page_table.shape[0] if cu_seqlens is None else _n_seqs(1, cu_seqlens)
     cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
     shape = (n if cu_seqlens is None else 1, int(T), k_cache.shape[2], k_cache.shape[3])
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s" % (name, list(shape)))
+    if (k_out is not None and k_out.shape != shape) or (v_out is not None and v_out.shape != shape):
+        raise ValueError("k_out and v_out must have shape %s" % list(shape))
     ts, tc = _index("start", start, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
-    _on_current_device(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
-                       start=start, cu_seqlens=cu_seqlens, k_out=k_out, v_out=v_out)
+    dev = _device_of(k_cache, v_cache, k_scale, v_scale, page_table, start, cu_seqlens, k_out, v_out)
     with _allocating_for(stream):
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+            k_out = k_cache.new_empty(shape, dtype=dtype)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
-    tk, tv = describe(k_out), describe(v_out)
-    st = lib.la_kv_read(ctypes.byref(cache), table, max_pages, ts, tc, n, ctypes.byref(tk), ctypes.byref(tv),
-                        _stream(stream))
+            v_out = k_out.new_empty(shape)
+    st = lib.la_kv_read(cache, table, max_pages, ts, tc, n, _describe(k_out), _describe(v_out), _stream_of(stream, dev))
     _check(lib, st, "la_kv_read")
     return k_out, v_out
 
@@ -724,29 +740,29 @@ def la_paged_attn(q, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_sc
     (see la_paged_attn in include/la_b200.h).  q [B,T,H,D]; kv_len int32 [N]; scale: D^-1/2 if None;
     window: 0 or the positions a query sees.  Returns (out, lse float32 [B,T,H] or None)."""
     lib = load_library()
-    tq = describe(q)
+    tq = _describe(q)
     B, T, H, D = q.shape
     n = _n_seqs(B, cu_seqlens)
     cache, (table, max_pages) = describe_cache(k_cache, v_cache, k_scale, v_scale), _table(page_table, n)
     tl, tc = _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, T, H) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 [B, T, H] tensor")
-    _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, kv_len=kv_len,
-                       page_table=page_table, cu_seqlens=cu_seqlens, out=out, lse=lse, workspace=workspace)
-    need = paged_attn_workspace_size(B, T, H, D, n, cu_seqlens is not None, cache.H, cache.page_size, k_cache.dtype,
-                                     q.dtype, flags)
+    dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, cu_seqlens, out, lse, workspace)
+    need = lib.la_paged_attn_workspace_size(B, T, H, D, n, tc is not None, cache.H, cache.page_size, cache.format,
+                                            tq.dtype, flags)
+    if need == _SIZE_MAX:
+        need = 0  # the call says what it refuses
     with _allocating_for(stream):
         if out is None:
-            out = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
+            out = q.new_empty((B, T, H, D))
         if lse is None and return_lse:
-            lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, T, H), dtype=torch.float32)
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    to = describe(out)
-    st = lib.la_paged_attn(ctypes.byref(tq), ctypes.byref(cache), table, max_pages, tl, tc, n,
-                           float(D ** -0.5 if scale is None else scale), int(window), ctypes.byref(to),
-                           None if lse is None else lse.data_ptr(), int(flags),
+            workspace = q.new_empty(need, dtype=torch.uint8)
+    st = lib.la_paged_attn(tq, cache, table, max_pages, tl, tc, n, D ** -0.5 if scale is None else scale, window,
+                           _describe(out), None if lse is None else lse.data_ptr(), flags,
                            None if workspace is None else workspace.data_ptr(),
-                           0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+                           0 if workspace is None else workspace.numel() * workspace.element_size(),
+                           _stream_of(stream, dev))
     _check(lib, st, "la_paged_attn")
     return out, lse
