@@ -80,130 +80,203 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
                                                    __NV_SATFINITE, __NV_E4M3);
       w[h] = lo | hi << 16;
     } else {
-      uint32_t b = 0;
+      // x 2^-e is exact, so adding 1.5 2^23 rounds it once, to nearest even, into the sum's low byte (|x 2^-e| <= 127).
+      // (A conversion instruction would run at an eighth of the rate.)
+      uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b |= ((uint32_t)__float2int_rn(f[4 * h + i] * inv) & 0xFFu) << (8 * i);
+      for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(fmaf(f[4 * h + i], inv, 12582912.f));
+      const uint32_t b = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
       w[h] = b;
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvMoveArgs a) {
-  const int lpr = a.c.D >> 3;  // threads of a row: a power of two <= 32
-  const uint32_t gid = blockIdx.x * (uint32_t)kKvThreads + threadIdx.x;
-  const uint32_t row = gid / lpr;
-  const int part = (int)(gid % lpr);
-  const uint32_t rows = (uint32_t)(a.B * a.T * a.c.H);
-  const bool in = row < rows;
-  const int64_t t = in ? row / (uint32_t)a.c.H : 0;
-  const int h = in ? (int)(row % (uint32_t)a.c.H) : 0;
-  int64_t n = 0, i = 0, L = 0;
-  bool live = in && locate(a.cu_seqlens, a.n_seqs, a.T, t, n, i, L);
-  const int64_t p = live ? (int64_t)a.pos[n] - L + i : -1;
-  const int64_t page = live ? page_of(a.c, n, p) : -1;
-  live = page >= 0;
-  float x[2][8];
-  if (live) {
-    const int64_t tb = a.cu_seqlens ? 0 : n, tt = a.cu_seqlens ? t : i;
-    load_row8((const T *)a.k.data + tb * a.k.sb + tt * a.k.st + h * a.k.sh + 8 * part, x[0]);
-    load_row8((const T *)a.v.data + tb * a.v.sb + tt * a.v.st + h * a.v.sh + 8 * part, x[1]);
-  } else {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) x[0][u] = x[1][u] = 0.f;
+// Where a token of the batch stands.  A block's threads look its few tokens up once (a search among the sequences and
+// a table entry, each a chain of loads) and leave them in shared memory for its rows.
+struct Place {
+  int64_t k, v;   // element offsets of its first head's dense rows
+  int64_t slot;   // page * page_size + slot in it, or -1: no slot
+  int32_t in;     // belongs to a sequence
+};
+
+template <bool WRITE>
+__device__ __forceinline__ void places(const KvMoveArgs &a, uint32_t first, uint32_t last, Place *tab) {
+  for (uint32_t t = first + threadIdx.x; t <= last; t += kKvThreads) {
+    Place p;
+    int64_t n, i, L;
+    p.slot = -1;
+    p.k = p.v = 0;
+    p.in = locate(a.cu_seqlens, a.n_seqs, a.T, t, n, i, L);
+    if (p.in) {
+      const int64_t tb = a.cu_seqlens ? 0 : n, tt = a.cu_seqlens ? (int64_t)t : i;
+      p.k = tb * a.k.sb + tt * a.k.st;
+      p.v = tb * a.v.sb + tt * a.v.st;
+      const int64_t at = WRITE ? (int64_t)a.pos[n] - L + i : (a.pos ? (int64_t)a.pos[n] : 0) + i;
+      const int64_t page = page_of(a.c, n, at);
+      if (page >= 0) p.slot = page * a.c.page_size + slot_of(a.c, at);
+    }
+    tab[t - first] = p;
   }
-  const int slot = live ? slot_of(a.c, p) : 0;
-  const int64_t off = live ? page * a.c.s_page + (int64_t)slot * a.c.s_tok + (int64_t)h * a.c.s_head + 8 * part : 0;
+  __syncthreads();
+}
+
+// A row of a block: its token's place, head, cache offset and scale index.
+struct Row {
+  int64_t k, v, off, scale;
+  bool in, live;
+};
+__device__ __forceinline__ Row row_at(const KvMoveArgs &a, const Place *tab, uint32_t first, uint32_t row, uint32_t rows) {
+  Row r;
+  r.k = r.v = r.off = r.scale = 0;
+  r.in = r.live = false;
+  if (row >= rows) return r;
+  const uint32_t t = row / (uint32_t)a.c.H, h = row - t * (uint32_t)a.c.H;
+  const Place p = tab[t - first];
+  r.in = p.in != 0;
+  r.k = p.k + (int64_t)h * a.k.sh;
+  r.v = p.v + (int64_t)h * a.v.sh;
+  if (p.slot >= 0) {
+    const int64_t page = (uint64_t)p.slot >> 32 ? p.slot / a.c.page_size : (int64_t)((uint32_t)p.slot / (uint32_t)a.c.page_size);
+    const int64_t slot = p.slot - page * a.c.page_size;
+    r.live = true;
+    r.off = page * a.c.s_page + slot * a.c.s_tok + (int64_t)h * a.c.s_head;
+    r.scale = (page * a.c.H + h) * (int64_t)a.c.page_size + slot;
+  }
+  return r;
+}
+
+// A block takes `turns` times its rows, one after the other; eight blocks share an SM and keep its loads under way.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kKvThreads, 8) kv_write_kernel(const KvMoveArgs a, int turns) {
+  extern __shared__ Place tab[];
+  const int lpr = a.c.D >> 3;  // threads of a row: a power of two <= 32
+  const int part = (int)(threadIdx.x % lpr);
+  const uint32_t rpb = kKvThreads / lpr, rows = (uint32_t)(a.B * a.T * a.c.H);
+  const uint32_t begin = blockIdx.x * rpb * turns, end = min(begin + rpb * turns, rows);
+  const uint32_t first = begin / (uint32_t)a.c.H;
+  places<true>(a, first, (end - 1) / (uint32_t)a.c.H, tab);
+#pragma unroll 1
+  for (uint32_t row = begin + threadIdx.x / lpr; row - threadIdx.x / lpr < end; row += rpb) {
+    const Row p = row_at(a, tab, first, row, end);
+    float x[2][8];
+    if (p.live) {
+      load_row8((const T *)a.k.data + p.k + 8 * part, x[0]);
+      load_row8((const T *)a.v.data + p.v + 8 * part, x[1]);
+    } else {
 #pragma unroll
-  for (int kvi = 0; kvi < 2; ++kvi) {
-    uint8_t *dst = kvi ? a.c.v : a.c.k;
+      for (int u = 0; u < 8; ++u) x[0][u] = x[1][u] = 0.f;
+    }
     if (FMT == LA_KV_BF16) {
-      if (live)
-        *reinterpret_cast<uint4 *>(dst + 2 * off) =
-            make_uint4(bf2(x[kvi][0], x[kvi][1]), bf2(x[kvi][2], x[kvi][3]), bf2(x[kvi][4], x[kvi][5]),
-                       bf2(x[kvi][6], x[kvi][7]));
+      if (p.live) {
+#pragma unroll
+        for (int kvi = 0; kvi < 2; ++kvi)
+          *reinterpret_cast<uint4 *>((kvi ? a.c.v : a.c.k) + 2 * (p.off + 8 * part)) =
+              make_uint4(bf2(x[kvi][0], x[kvi][1]), bf2(x[kvi][2], x[kvi][3]), bf2(x[kvi][4], x[kvi][5]),
+                         bf2(x[kvi][6], x[kvi][7]));
+      }
       continue;
     }
     // magnitudes compare as unsigned bit patterns; infinities and NaN come out on top
-    uint32_t m = 0;
+    uint32_t m[2] = {0, 0};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(x[kvi][u]) & 0x7FFFFFFFu);
-    for (int o = 1; o < lpr; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (live) {
-      const bool finite = m < 0x7F800000u;
-      const int e = finite ? scale_exp<FMT>(m) : 0;
-      const uint2 code = finite ? encode8<FMT>(x[kvi], __uint_as_float((uint32_t)(127 - e) << 23)) : make_uint2(0, 0);
-      *reinterpret_cast<uint2 *>(dst + off) = code;
-      if (part == 0)
-        (kvi ? a.c.vs : a.c.ks)[(page * a.c.H + h) * (int64_t)a.c.page_size + slot] =
-            finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+    for (int kvi = 0; kvi < 2; ++kvi)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) m[kvi] = max(m[kvi], __float_as_uint(x[kvi][u]) & 0x7FFFFFFFu);
+    if (sizeof(T) == 2) {  // bf16 magnitudes fill 16 bits: both rows' maxima in one word
+      uint32_t both = (m[1] & 0xFFFF0000u) | (m[0] >> 16);
+      for (int o = 1; o < lpr; o <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+      m[0] = both << 16;
+      m[1] = both & 0xFFFF0000u;
+    } else {
+      for (int o = 1; o < lpr; o <<= 1) {
+        m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        m[1] = max(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+      }
+    }
+    if (p.live) {
+#pragma unroll
+      for (int kvi = 0; kvi < 2; ++kvi) {
+        const bool finite = m[kvi] < 0x7F800000u;
+        const int e = finite ? scale_exp<FMT>(m[kvi]) : 0;
+        const uint2 code = finite ? encode8<FMT>(x[kvi], __uint_as_float((uint32_t)(127 - e) << 23)) : make_uint2(0, 0);
+        *reinterpret_cast<uint2 *>((kvi ? a.c.v : a.c.k) + p.off + 8 * part) = code;
+        if (part == 0)
+          (kvi ? a.c.vs : a.c.ks)[p.scale] =
+              finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+      }
     }
   }
 }
 
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvMoveArgs a) {
+__global__ void __launch_bounds__(kKvThreads, 8) kv_read_kernel(const KvMoveArgs a, int turns) {
+  extern __shared__ Place tab[];
   const int lpr = a.c.D >> 3;
-  const uint32_t gid = blockIdx.x * (uint32_t)kKvThreads + threadIdx.x;
-  const uint32_t row = gid / lpr;
-  const int part = (int)(gid % lpr);
-  if (row >= (uint32_t)(a.B * a.T * a.c.H)) return;
-  const int64_t t = row / (uint32_t)a.c.H;
-  const int h = (int)(row % (uint32_t)a.c.H);
-  int64_t n = 0, i = 0, L = 0;
-  if (!locate(a.cu_seqlens, a.n_seqs, a.T, t, n, i, L)) return;
-  const int64_t p = (a.pos ? (int64_t)a.pos[n] : 0) + i;
-  const int64_t page = page_of(a.c, n, p);
-  const int64_t tb = a.cu_seqlens ? 0 : n, tt = a.cu_seqlens ? t : i;
-  float x[2][8];
+  const int part = (int)(threadIdx.x % lpr);
+  const uint32_t rpb = kKvThreads / lpr, rows = (uint32_t)(a.B * a.T * a.c.H);
+  const uint32_t begin = blockIdx.x * rpb * turns, end = min(begin + rpb * turns, rows);
+  const uint32_t first = begin / (uint32_t)a.c.H;
+  places<false>(a, first, (end - 1) / (uint32_t)a.c.H, tab);
+#pragma unroll 1
+  for (uint32_t row = begin + threadIdx.x / lpr; row < end; row += rpb) {
+    const Row p = row_at(a, tab, first, row, end);
+    if (!p.in) continue;
+    float x[2][8];
+    if (p.live) {
+      load8<FMT>(a.c.k + elem_bytes(FMT) * (p.off + 8 * part), x[0]);
+      load8<FMT>(a.c.v + elem_bytes(FMT) * (p.off + 8 * part), x[1]);
+      if (FMT != LA_KV_BF16) {
+        const float ks = a.c.ks[p.scale], vs = a.c.vs[p.scale];
 #pragma unroll
-  for (int kvi = 0; kvi < 2; ++kvi)
+        for (int u = 0; u < 8; ++u) x[0][u] *= ks, x[1][u] *= vs;
+      }
+    } else {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) x[kvi][u] = 0.f;
-  if (page >= 0) {
-    const int slot = slot_of(a.c, p);
-    const int64_t off = page * a.c.s_page + (int64_t)slot * a.c.s_tok + (int64_t)h * a.c.s_head + 8 * part;
-    load8<FMT>(a.c.k + elem_bytes(FMT) * off, x[0]);
-    load8<FMT>(a.c.v + elem_bytes(FMT) * off, x[1]);
-    if (FMT != LA_KV_BF16) {
-      const int64_t so = (page * a.c.H + h) * (int64_t)a.c.page_size + slot;
-      const float ks = a.c.ks[so], vs = a.c.vs[so];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[0][u] *= ks, x[1][u] *= vs;
+      for (int u = 0; u < 8; ++u) x[0][u] = x[1][u] = 0.f;
     }
+    store_row8((T *)a.k.data + p.k + 8 * part, x[0]);
+    store_row8((T *)a.v.data + p.v + 8 * part, x[1]);
   }
-  store_row8((T *)a.k.data + tb * a.k.sb + tt * a.k.st + h * a.k.sh + 8 * part, x[0]);
-  store_row8((T *)a.v.data + tb * a.v.sb + tt * a.v.st + h * a.v.sh + 8 * part, x[1]);
 }
 
-unsigned kv_blocks(const KvMoveArgs &a) {
-  const int64_t threads = a.B * a.T * a.c.H * (a.c.D / 8);
-  return (unsigned)((threads + kKvThreads - 1) / kKvThreads);
+// Eight turns a block where that still leaves eight blocks an SM, else one.
+template <template <typename, int> class K>
+cudaError_t launch(const KvMoveArgs &a, cudaStream_t stream) {
+  const int64_t rows = a.B * a.T * a.c.H;
+  const int64_t rpb = kKvThreads / (a.c.D / 8);
+  const int turns = rows >= rpb * 8 * 8 * 148 ? 8 : 1;
+  const unsigned grid = (unsigned)((rows + rpb * turns - 1) / (rpb * turns));
+  const size_t smem = (size_t)((rpb * turns - 1) / a.c.H + 2) * sizeof(Place);
+  const bool bf = a.dtype == LA_BF16;
+  switch (a.c.format) {
+    case LA_KV_E4M3:
+      bf ? K<__nv_bfloat16, LA_KV_E4M3>::go(a, grid, turns, smem, stream) : K<float, LA_KV_E4M3>::go(a, grid, turns, smem, stream);
+      break;
+    case LA_KV_INT8:
+      bf ? K<__nv_bfloat16, LA_KV_INT8>::go(a, grid, turns, smem, stream) : K<float, LA_KV_INT8>::go(a, grid, turns, smem, stream);
+      break;
+    default:
+      bf ? K<__nv_bfloat16, LA_KV_BF16>::go(a, grid, turns, smem, stream) : K<float, LA_KV_BF16>::go(a, grid, turns, smem, stream);
+  }
+  return cudaGetLastError();
 }
+template <typename T, int FMT>
+struct Write {
+  static void go(const KvMoveArgs &a, unsigned grid, int turns, size_t smem, cudaStream_t st) {
+    kv_write_kernel<T, FMT><<<grid, kKvThreads, smem, st>>>(a, turns);
+  }
+};
+template <typename T, int FMT>
+struct Read {
+  static void go(const KvMoveArgs &a, unsigned grid, int turns, size_t smem, cudaStream_t st) {
+    kv_read_kernel<T, FMT><<<grid, kKvThreads, smem, st>>>(a, turns);
+  }
+};
 
 }  // namespace
 
-cudaError_t launch_kv_write(const KvMoveArgs &a, cudaStream_t stream) {
-  const unsigned grid = kv_blocks(a);
-#define LA_KV_LAUNCH(K, FMT)                                                       \
-  do {                                                                             \
-    if (a.dtype == LA_BF16) K<__nv_bfloat16, FMT><<<grid, kKvThreads, 0, stream>>>(a); \
-    else K<float, FMT><<<grid, kKvThreads, 0, stream>>>(a);                        \
-  } while (0)
-  if (a.c.format == LA_KV_E4M3) LA_KV_LAUNCH(kv_write_kernel, LA_KV_E4M3);
-  else if (a.c.format == LA_KV_INT8) LA_KV_LAUNCH(kv_write_kernel, LA_KV_INT8);
-  else LA_KV_LAUNCH(kv_write_kernel, LA_KV_BF16);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_kv_read(const KvMoveArgs &a, cudaStream_t stream) {
-  const unsigned grid = kv_blocks(a);
-  if (a.c.format == LA_KV_E4M3) LA_KV_LAUNCH(kv_read_kernel, LA_KV_E4M3);
-  else if (a.c.format == LA_KV_INT8) LA_KV_LAUNCH(kv_read_kernel, LA_KV_INT8);
-  else LA_KV_LAUNCH(kv_read_kernel, LA_KV_BF16);
-#undef LA_KV_LAUNCH
-  return cudaGetLastError();
-}
+cudaError_t launch_kv_write(const KvMoveArgs &a, cudaStream_t stream) { return launch<Write>(a, stream); }
+cudaError_t launch_kv_read(const KvMoveArgs &a, cudaStream_t stream) { return launch<Read>(a, stream); }
 
 }  // namespace la
