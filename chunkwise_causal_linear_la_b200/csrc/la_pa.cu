@@ -297,7 +297,8 @@ struct PaCfg {
                        B_OEMPTY = B_QFULL + 8, B_MERGE = B_QFULL + 10, B_DRAIN = B_QFULL + 11,
                        B_PSPLIT = B_QFULL + 12, B_ODONE = B_QFULL + 14,  // one query tile: P of both groups; PV done
                        B_PHALF = B_QFULL + 15,  // two query tiles: P's second half (PFULL: the first)
-                       B_READY = B_QFULL + 17,  // bf16, per slot: fixed up
+                       B_HDONE = B_QFULL + 17,  // ... PV of the first half done
+                       B_READY = B_QFULL + 19,  // bf16, per slot: fixed up
                        NBAR = B_READY + (Q8 ? 0 : NS);
   // per item (mod 16) and fix-up or conversion warp: values that are not finite were taken out.  (A flag left
   // from 16 items before only costs a look for such values.)
@@ -392,6 +393,25 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^(s c + b) of two scores, and pairwise sums: two products or sums an instruction.
+__device__ __forceinline__ float2 weight2(float s0, float s1, float c, float b) {
+  float2 x;
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmov.b64 w, {%5, %5};\n\t"
+      "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(x.x), "=f"(x.y)
+      : "f"(s0), "f"(s1), "f"(c), "f"(b));
+  x.x = ex2(x.x);
+  x.y = ex2(x.y);
+  return x;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 // Sixteen codes times the scale f as bf16.
@@ -646,6 +666,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   for (int kk = 0; kk < kTile / 32; ++kk)
                     umma_bf16_ts(tbase + G::T_O + w * D, tbase + G::T_S + w * kTile + hf * 32 + kk * 8,
                                  dv + (((hf * 4 + kk) * 2048) >> 4), ID_PV, (i > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                  if (hf == 0) umma_commit(bars + G::B_HDONE + w);
                 }
                 __syncwarp();
               }
@@ -759,8 +780,8 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t ts_addr = tbase + G::T_S + lane_off;
     const uint32_t to_addr = tbase + G::T_O + lane_off;
-    const float c = a.c, thr = 8.f / c;
-    uint32_t scnt[2] = {0, 0}, ocnt[2] = {0, 0}, mcnt = 0, dcnt = 0, items = 0;
+    const float c = a.c;
+    uint32_t scnt[2] = {0, 0}, ocnt[2] = {0, 0}, mcnt = 0, dcnt = 0, hcnt = 0, items = 0;
     bool ok = true;
     while (ok && walk.next(a, it)) {
       const bool two = NQ == 2 && it.e.ntok > a.tpt;
@@ -774,91 +795,97 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       int lo, hi;
       sees(a, it.e, tk, lo, hi);
       if (!valid) lo = hi = 0;
-      float m = -INFINITY, l = 0.f;
+      // tiles [full0, full1) of the piece: every token of the entry sees all of their keys
+      int full0, full1;
+      {
+        int x, lo1, hi0, y;
+        sees(a, it.e, 0, x, hi0);
+        sees(a, it.e, max(it.e.ntok, 1) - 1, lo1, y);
+        full0 = (lo1 + kTile - 1) / kTile - it.t0;
+        full1 = max(hi0, 0) / kTile - it.t0;
+      }
+      float m = -INFINITY, l = 0.f;  // the maximum in powers of two: scale log2(e) times the score
       if (two) {
-        // ---- this group's query tile: a lane is a row
+        // ---- this group's query tile: a lane is a row.  64 keys at a time; P's columns [32 h, 32 h + 32) lie over S's,
+        // which are read by then.  The weights are worked out with the maximum as it stands while the keys' own is
+        // found; where that is more than 8 above it (seldom after the first keys) O and l are rescaled and they are
+        // worked out anew.
         const uint32_t sw = ts_addr + w * kTile, ow = to_addr + w * D;
         for (int i = 0; i < it.n && part_of; ++i) {
           if (!(ok = wait_on_warp(sy, G::B_SFULL + w, (scnt[w] + i) & 1, it.t0 + i))) break;
           if (active) {
             tc_fence_after();
-              // Two passes over S, 64 columns at a time (a second read of tensor memory costs less than the registers
-              // and the straight-line code of holding 128 columns): the row's maximum, then the weights.  P's columns
-              // [32 h, 32 h + 32) lie over S's, which are read by then.
-              const int va = in_tile(lo, (it.t0 + i) * kTile), vb = in_tile(hi, (it.t0 + i) * kTile);
-              const uint32_t width = (uint32_t)max(vb - va, 0);
-              const bool masked = __any_sync(0xffffffffu, va > 0 || vb < kTile);
+            const bool masked = i < full0 || i >= full1;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
               uint32_t s[2][32];
-              auto load_half = [&](int hf) {
-                tmem_ld_32x32b_x32(sw + 64 * hf, s[0]);
-                tmem_ld_32x32b_x32(sw + 64 * hf + 32, s[1]);
-                tmem_wait_ld();
-                if (masked) {
-                  const int base = 64 * hf - va;
+              tmem_ld_32x32b_x32(sw + 64 * hf, s[0]);
+              tmem_ld_32x32b_x32(sw + 64 * hf + 32, s[1]);
+              tmem_wait_ld();
+              if (masked) {
+                const int ts = (it.t0 + i) * kTile + 64 * hf;
+                const int va = min(max(lo - ts, 0), 64), vb = min(max(hi - ts, 0), 64);
+                const uint32_t width = (uint32_t)max(vb - va, 0);
 #pragma unroll
-                  for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                      if ((uint32_t)(base + 32 * q + j) >= width) s[q][j] = 0xFF800000u;
-                }
-              };
-              float mx = -INFINITY;
-#pragma unroll 1
-              for (int hf = 0; hf < 2; ++hf) {
-                load_half(hf);
-                float m4[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  m4[x] = __uint_as_float(s[x >> 1][16 * (x & 1)]);
-#pragma unroll
-                  for (int j = 1; j < 16; ++j) m4[x] = fmaxf(m4[x], __uint_as_float(s[x >> 1][16 * (x & 1) + j]));
-                }
-                mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                  for (int j = 0; j < 32; ++j)
+                    if ((uint32_t)(32 * q + j - va) >= width) s[q][j] = 0xFF800000u;
               }
-              if (m == -INFINITY) m = mx;  // nothing summed yet: O's row is not there, or zero
-              const bool up = mx > m + thr;
-              if (__any_sync(0xffffffffu, up)) {
-                const float f = up ? ex2((m - mx) * c) : 1.f;
-                if (up) m = mx;
-                l *= f;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                  uint32_t o[32];
-                  tmem_ld_32x32b_x32(ow + 32 * q, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                  tmem_st_32x32b_x32(ow + 32 * q, o);
-                }
-              }
-              const float mc = m == -INFINITY ? 0.f : m * c;
-              float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-              for (int hf = 0; hf < 2; ++hf) {
-                load_half(hf);
-                uint32_t p[32];
+              uint32_t p[32];
+              float sum;
+              while (true) {
+                const float base = m == -INFINITY ? 0.f : m;
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  const int q = j >> 4, k = 2 * (j & 15);
-                  const float x = ex2(fmaf(__uint_as_float(s[q][k]), c, -mc));
-                  const float y = ex2(fmaf(__uint_as_float(s[q][k + 1]), c, -mc));
-                  l4[j & 1] += x;
-                  l4[2 + (j & 1)] += y;
-                  p[j] = pack2(x, y);
+                  const float s0 = __uint_as_float(s[j >> 4][2 * (j & 15)]), s1 = __uint_as_float(s[j >> 4][2 * (j & 15) + 1]);
+                  const float2 x = weight2(s0, s1, c, -base);
+                  l2[j & 1] = add2(l2[j & 1], x);
+                  m4[2 * (j & 1)] = fmaxf(m4[2 * (j & 1)], s0);
+                  m4[2 * (j & 1) + 1] = fmaxf(m4[2 * (j & 1) + 1], s1);
+                  p[j] = pack2(x.x, x.y);
                 }
-                tmem_st_32x32b_x32(sw + 32 * hf, p);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_n(bars + (hf ? G::B_PHALF : G::B_PFULL) + w, quad == 0 ? 1 + idle : 1);
+                sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+                const bool up = mx > m + 8.f;
+                if (!__any_sync(0xffffffffu, up)) break;
+                const float f = up ? ex2(m - mx) : 1.f;
+                if (up) m = mx;
+                l *= f;
+                if (i > 0 || hf > 0) {  // O has all but this half's keys (the tile's first half: wait for its product)
+                  if (hf > 0 && !wait_on_warp(sy, G::B_HDONE + w, (hcnt + i) & 1, it.t0 + i)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(ow + 32 * q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st_32x32b_x32(ow + 32 * q, o);
+                  }
+                }
               }
-              l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+              l += sum;
+              tmem_st_32x32b_x32(sw + 32 * hf, p);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_n(bars + (hf ? G::B_PHALF : G::B_PFULL) + w, quad == 0 ? 1 + idle : 1);
+            }
           } else if (lane == 0) {
             arrive_n(bars + G::B_PFULL + w, 4);
             arrive_n(bars + G::B_PHALF + w, 4);
           }
           __syncwarp();
+          if (!ok) break;
         }
+        hcnt += it.n;
         scnt[0] += it.n;
         scnt[1] += it.n;
       } else {
@@ -893,87 +920,77 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           if (active) {
             tc_fence_after();
             const int ts = (it.t0 + i) * kTile;
+            const bool masked = i < full0 || i >= full1;
 #pragma unroll
             for (int x = 0; x < XH; ++x) {
               if (!act[x]) continue;
               uint32_t s[32];
               const uint32_t at = ts_addr + b * kTile + 64 * w + ((uint32_t)(16 * x) << 16);
               tmem_ld_16x256b_x8(at, s);
-              int va[2], vb[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                va[y] = min(max(rlo[x][y] - ts, 0), 64);
-                vb[y] = min(max(rhi[x][y] - ts, 0), 64);
-              }
-              const bool part = va[0] > 0 || va[1] > 0 || vb[0] < 64 || vb[1] < 64;
               tmem_wait_ld();
-              if (__any_sync(0xffffffffu, part)) {
+              if (masked) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const int base = 2 * (lane & 3) - va[y];
-                  const uint32_t width = (uint32_t)max(vb[y] - va[y], 0);
+                  const int va = min(max(rlo[x][y] - ts, 0), 64), vb = min(max(rhi[x][y] - ts, 0), 64);
+                  const int base = 2 * (lane & 3) - va;
+                  const uint32_t width = (uint32_t)max(vb - va, 0);
 #pragma unroll
                   for (int k = 0; k < 16; ++k)
                     if ((uint32_t)(base + 8 * (k >> 1) + (k & 1)) >= width) s[4 * (k >> 1) + 2 * y + (k & 1)] = 0xFF800000u;
                 }
               }
-              float mx[2], f[2];
-              bool up = false;
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float e0 = __uint_as_float(s[2 * y]), e1 = __uint_as_float(s[2 * y + 1]);
-#pragma unroll
-                for (int k = 1; k < 8; ++k) {
-                  e0 = fmaxf(e0, __uint_as_float(s[4 * k + 2 * y]));
-                  e1 = fmaxf(e1, __uint_as_float(s[4 * k + 2 * y + 1]));
-                }
-                mx[y] = fmaxf(e0, e1);
-              }
-#pragma unroll
-              for (int o = 1; o < 4; o <<= 1) {
-                const float y0 = __shfl_xor_sync(0xffffffffu, mx[0], o), y1 = __shfl_xor_sync(0xffffffffu, mx[1], o);
-                mx[0] = fmaxf(mx[0], y0);
-                mx[1] = fmaxf(mx[1], y1);
-              }
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                if (hm[x][y] == -INFINITY) hm[x][y] = mx[y];  // nothing summed yet: O's row is not there, or zero
-                const bool u = mx[y] > hm[x][y] + thr;
-                f[y] = u ? ex2((hm[x][y] - mx[y]) * c) : 1.f;
-                if (u) hm[x][y] = mx[y];
-                up = up || u;
-              }
-              if (__any_sync(0xffffffffu, up)) {  // O must hold the tile before
-                if (!wait_on_warp(sy, G::B_ODONE, (dcnt - 1) & 1, it.t0 + i)) ok = false;
-                tc_fence_after();
-                hl[x][0] *= f[0];
-                hl[x][1] *= f[1];
-#pragma unroll 1
-                for (int q = 0; q < D / 64; ++q) {
-                  uint32_t o[32];
-                  const uint32_t oa = to_addr + ((uint32_t)(16 * x) << 16) + w * D + 64 * q;
-                  tmem_ld_16x256b_x8(oa, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
-                  tmem_st_16x256b_x8(oa, o);
-                }
-              }
               uint32_t p[16];
+              float sum[2];
+              while (true) {  // as above; a row's maximum is its four lanes' where it has to be known
+                float mx[2];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float mc = hm[x][y] == -INFINITY ? 0.f : hm[x][y] * c;
-                float la = 0.f, lb = 0.f;
+                for (int y = 0; y < 2; ++y) {
+                  const float base = hm[x][y] == -INFINITY ? 0.f : hm[x][y];
+                  float2 l2 = make_float2(0.f, 0.f);
+                  float e0 = -INFINITY, e1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float x0 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * y]), c, -mc));
-                  const float x1 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * y + 1]), c, -mc));
-                  la += x0;
-                  lb += x1;
-                  p[2 * k + y] = pack2(x0, x1);
+                  for (int k = 0; k < 8; ++k) {
+                    const float s0 = __uint_as_float(s[4 * k + 2 * y]), s1 = __uint_as_float(s[4 * k + 2 * y + 1]);
+                    const float2 v = weight2(s0, s1, c, -base);
+                    l2 = add2(l2, v);
+                    e0 = fmaxf(e0, s0);
+                    e1 = fmaxf(e1, s1);
+                    p[2 * k + y] = pack2(v.x, v.y);
+                  }
+                  sum[y] = l2.x + l2.y;
+                  mx[y] = fmaxf(e0, e1) * c;
                 }
-                hl[x][y] += la + lb;
+                if (!__any_sync(0xffffffffu, mx[0] > hm[x][0] + 8.f || mx[1] > hm[x][1] + 8.f)) break;
+                float f[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
+                  mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
+                  const bool up = mx[y] > hm[x][y] + 8.f;
+                  f[y] = up ? ex2(hm[x][y] - mx[y]) : 1.f;
+                  if (up) hm[x][y] = mx[y];
+                  hl[x][y] *= f[y];
+                }
+                if (i > 0) {  // O must hold the tile before
+                  if (!wait_on_warp(sy, G::B_ODONE, (dcnt - 1) & 1, it.t0 + i)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int q = 0; q < D / 64; ++q) {
+                    uint32_t o[32];
+                    const uint32_t oa = to_addr + ((uint32_t)(16 * x) << 16) + w * D + 64 * q;
+                    tmem_ld_16x256b_x8(oa, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                    tmem_st_16x256b_x8(oa, o);
+                  }
+                }
               }
+              hl[x][0] += sum[0];
+              hl[x][1] += sum[1];
               tmem_st_16x128b_x8(at, p);
             }
             tmem_wait_st();
@@ -996,7 +1013,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       }
       if (!ok) break;
       // ------------------------------------------------------------------ epilogue
-      const float mc = m * c;
+      const float mc = m;
       const bool mine = two || w == 0;
       if (!mine) {  // O[1] complete: the previous item's statistics have been read
         if (!(ok = part_of ? wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0)
