@@ -41,6 +41,7 @@
 // returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "la_common.cuh"
@@ -414,15 +415,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// Sixteen codes times the scale f as bf16.
-//   e4m3: exponent and mantissa bits moved to bf16's places, value 2^-120 of the code's; the product with
-//         2^120 is exact (bf16 keeps subnormals), and so is the one with a power-of-two scale.  For scales up to
-//         2^7 (2^120 f is a bf16 then) the two are one.
-//   int8: with the low 7 bits L and the sign bit S, (128 + L) - (128 + 128 S) by bit patterns of bf16.
-__device__ __forceinline__ uint32_t mul2(uint32_t v, __nv_bfloat162 f) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&v), f);
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
+// Sixteen codes times the scale f as bf16 (exact for the powers of two that la_kv_write stores).
+//   e4m3: the hardware's conversion of pairs to fp16 (exact), fp32 products, one rounding.
+//   int8: with the low 7 bits L and the sign bit S of a code, p = 128 + L and q = 128 + 128 S by bit patterns of
+//         bf16, and p f - q f in one fused step (q f is exact).  q f overflows where f exceeds 2^118: the difference
+//         is taken first there.
+// Instructions on bits run at half rate, which bounds the conversion: per pair of codes these take two and a half to
+// three (moving e4m3's bits into bf16's places would take four).
 template <int FMT>
 __device__ __forceinline__ void convert16(const uint4 &w, float f, uint4 &o0, uint4 &o1) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -430,30 +429,47 @@ __device__ __forceinline__ void convert16(const uint4 &w, float f, uint4 &o0, ui
   if (FMT == LA_KV_E4M3) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t b = __byte_perm(in[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
-      v[k] = ((b >> 4) & 0x07F007F0u) | (b & 0x80008000u);
-    }
-    const bool wide = f > 128.f;
-    const __nv_bfloat162 f2 = __float2bfloat162_rn((wide ? 1.f : f) * 1.329227995784916e36f);  // 2^120
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], f2);
-    if (__any_sync(0xffffffffu, wide)) {
-      const __nv_bfloat162 g2 = __float2bfloat162_rn(wide ? f : 1.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], g2);
+      const uint32_t pair = k & 1 ? in[k >> 1] >> 16 : in[k >> 1] & 0xFFFFu;
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
+      const float2 g = __half22float2(__half2(h));
+      v[k] = pack2(g.x * f, g.y * f);
     }
   } else {
-    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+    const bool wide = f > 3.32306998946228968e35f;  // 2^118
+    const __nv_bfloat162 f2 = __float2bfloat162_rn(wide ? 1.f : f), nf = __float2bfloat162_rn(wide ? -1.f : -f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint32_t b = __byte_perm(in[k >> 1], 0, k & 1 ? 0x4342 : 0x4140);
-      const uint32_t p = (b & 0x007F007Fu) | 0x43004300u, q = (b & 0x00800080u) | 0x43004300u;
-      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&p), *reinterpret_cast<const __nv_bfloat162 *>(&q));
-      v[k] = mul2(*reinterpret_cast<const uint32_t *>(&r), f2);
+      uint32_t p, q;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(p) : "r"(b), "r"(0x007F007Fu), "r"(0x43004300u));
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q) : "r"(b), "r"(0x00800080u), "r"(0x43004300u));
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&p), f2,
+                                       __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&q), nf));
+      v[k] = *reinterpret_cast<const uint32_t *>(&r);
+    }
+    if (__any_sync(0xffffffffu, wide)) {
+      const __nv_bfloat162 g2 = __float2bfloat162_rn(wide ? f : 1.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v[k]), g2);
+        v[k] = *reinterpret_cast<const uint32_t *>(&r);
+      }
     }
   }
   o0 = make_uint4(v[0], v[1], v[2], v[3]);
   o1 = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// Takes e4m3's NaN codes out of a word.
+__device__ __forceinline__ uint32_t keep_numbers(uint32_t w) { return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at));
+  return u;
+}
+__device__ __forceinline__ void sts16(uint32_t at, const uint4 &u) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
 }
 
 __device__ __forceinline__ bool finite_f(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
@@ -1083,10 +1099,11 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                 const int sl = (int)(p % a.page_size);
                 const int64_t off = (int64_t)pg * a.s_page + (int64_t)sl * a.s_tok + (int64_t)it.head * a.s_head + 32 * q;
                 const float vs = G::Q8 ? a.vs[((int64_t)pg * a.Hkv + it.head) * a.page_size + sl] : 0.f;
-                if (G::Q8 && finite_f(vs)) continue;
+                if (FMT == LA_KV_INT8 && finite_f(vs)) continue;
 #pragma unroll
                 for (int u = 0; u < 32; ++u) {
                   float v = vs * 0.f;  // a scale that is not finite: NaN
+                  if (FMT == LA_KV_E4M3 && (a.v[off + u] & 0x7F) == 0x7F) v = __uint_as_float(0x7FC00000u);
                   if (!G::Q8) v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.v)[off + u]);
                   if (!finite_f(v)) o[u] += v;
                 }
@@ -1191,12 +1208,12 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     reg_dealloc<G::R_CONV>();
     // ---------------------------------------------------------------- conversion
     constexpr int NRr = G::NR > 0 ? G::NR : 1;
-    // Work is cut into passes of 16 codes a lane.  D = 128 (codes under the 128-byte swizzle): two pairs of rows a,
-    // a ^ 5 of an 8-row group; eight lanes take half a row of each of a pair, which spreads both their 16-byte reads
-    // and their 16-byte writes over all banks; the group's other four rows are a ^ 2.  D = 64 (plain rows of 64
-    // bytes): the 8 rows of a group.
-    // Every other four warps take the keys, the others the values: a set's waits and fences pass while the other works.
-    constexpr int PASSES = D == 128 ? 32 : 16, SET = G::Q8 ? G::CONV / 2 : 8, W0 = SET / 4;
+    // Work is cut into turns of two times 16 codes a lane.  D = 128 (codes under the 128-byte swizzle), an 8-row group: two
+    // pairs of rows a, a ^ 5 and the other four rows, a ^ 2; eight lanes take half a row of each of a pair, which
+    // spreads both their 16-byte reads and their 16-byte writes over all banks.  D = 64 (plain rows of 64 bytes): two
+    // 8-row groups.  Every other four warps take the keys, the others the values: a set's waits and fences pass while
+    // the other works.
+    constexpr int TURNS = D == 128 ? 16 : 8, SET = G::Q8 ? G::CONV / 2 : 8;
     const int q4 = lane & 3, slab = D == 128 ? (lane >> 3) & 1 : 0, cw = warp - 12;
     const int kvi = (cw >> 2) & 1, ci = (cw & 3) + 4 * (cw >> 3);
     const int r8 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
@@ -1209,50 +1226,59 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       if (lane == 0) bad[(items & 15) * 16 + cw] = 0;
       __syncwarp();
       // Even shares beside two full softmax groups.  When the rows are few all of the softmax runs on the first quarter
-      // of the SM (the first rows belong to its warps): the conversion warps there take a sixteenth together.
+      // of the SM (the first rows belong to its warps): the conversion warps there take an eighth together.
       const bool even = D == 64 || it.e.ntok * a.g > G::WROWS;
-      constexpr int P0 = PASSES / 16 / W0, P1 = (PASSES - W0 * P0) / (SET - W0);
-      const int few = (ci & 3) == 0 ? (ci >> 2) * P0 : W0 * P0 + (ci - 1 - (ci >> 2)) * P1;
-      const int first = even ? ci * (PASSES / SET) : few;
-      const int last = first + (even ? PASSES / SET : (ci & 3) == 0 ? P0 : P1);
+      const int first = even ? ci * (TURNS / SET) : ((SET == 8 ? 0xDB917520u : 0xC720u) >> (4 * ci)) & 15;
+      const int last = first + (even ? TURNS / SET : ((SET == 8 ? 0x32212231u : 0x4552u) >> (4 * ci)) & 15);
       for (int i = 0; i < it.n && ok; ++i) {
         const Reach rc = reach(a, it.e, it.t0 + i);
         const bool part = partly(rc);
         {
           if (!(ok = wait_on_warp(sy, G::B_RFULL + rs, rph, it.t0 + i))) break;
-          // pass u: rows of group u / 2, the upper or lower four (D = 128), or of group u
-          const uint8_t *src = raw_stage(rs);
-          const float *ss = sc + rs * kTile;
-          auto codes_at = [&](int u) {
-            return *reinterpret_cast<const uint4 *>(src + (D == 128 ? (u >> 1) * 1024 + (soff ^ ((u & 1) * 0x120)) : u * 512 + soff));
-          };
-          auto row_of = [&](int u) { return D == 128 ? (u >> 1) * 8 + (r8 ^ ((u & 1) * 2)) : u * 8 + r8; };
-          uint4 nw = codes_at(first);
-          float nf = ss[row_of(first)];
           if (!(ok = wait_on_warp(sy, G::B_EMPTY + os, oph, it.t0 + i))) break;
-          uint8_t *dst = op_slot(os);
+          const uint32_t src = smem_u32(raw_stage(rs)) + soff, dst = smem_u32(op_slot(os)) + doff;
+          const float *ss = sc + rs * kTile + r8;
           int found = 0;
 #pragma unroll 1
           for (int u = first; u < last; ++u) {
-            const uint4 w = nw;
-            float f = nf;
-            const int row = row_of(u);
-            if (u + 1 < last) {  // ahead of this pass's stores
-              nw = codes_at(u + 1);
-              nf = ss[row_of(u + 1)];
+            uint4 w[2];
+            float f[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              w[x] = lds16(D == 128 ? (src + u * 1024) ^ (x * 0x120) : src + u * 1024 + x * 512);
+              f[x] = D == 128 ? *reinterpret_cast<const float *>(reinterpret_cast<uintptr_t>(ss + u * 8) ^ (x * 8))
+                              : ss[u * 16 + x * 8];
             }
             if (part) {
-              if (row < rc.a || row >= rc.d) f = 0.f;  // seen by none (codes are finite by construction)
-              if (kvi && !finite_f(f) && (row < rc.b || row >= rc.c)) {
-                f = 0.f;
-                found = 1;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int row = D == 128 ? u * 8 + (r8 ^ (x * 2)) : u * 16 + x * 8 + r8;
+                if (row < rc.a || row >= rc.d) {  // seen by none, whatever it holds
+                  w[x] = make_uint4(0, 0, 0, 0);
+                  f[x] = 0.f;
+                }
+                if (kvi && (row < rc.b || row >= rc.c)) {
+                  if (!finite_f(f[x])) {
+                    f[x] = 0.f;
+                    found = 1;
+                  }
+                  if (FMT == LA_KV_E4M3) {
+                    const uint4 n = make_uint4(keep_numbers(w[x].x), keep_numbers(w[x].y), keep_numbers(w[x].z),
+                                               keep_numbers(w[x].w));
+                    if (n.x != w[x].x || n.y != w[x].y || n.z != w[x].z || n.w != w[x].w) found = 1;
+                    w[x] = n;
+                  }
+                }
               }
             }
-            uint4 o0, o1;
-            convert16<FMT>(w, f, o0, o1);
-            const int at = D == 128 ? (u >> 1) * 1024 + (doff ^ ((u & 1) * 0x120)) : u * 1024 + doff;
-            *reinterpret_cast<uint4 *>(dst + at) = o0;
-            *reinterpret_cast<uint4 *>(dst + (at ^ 16)) = o1;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint4 o0, o1;
+              convert16<FMT>(w[x], f[x], o0, o1);
+              const uint32_t at = D == 128 ? (dst + u * 1024) ^ (x * 0x120) : dst + u * 2048 + x * 1024;
+              sts16(at, o0);
+              sts16(at ^ 16, o1);
+            }
           }
           if (found) bad[(items & 15) * 16 + cw] = 1;
           fence_proxy_async_smem();
