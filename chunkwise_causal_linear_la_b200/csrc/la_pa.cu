@@ -416,12 +416,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // Sixteen codes times the scale f as bf16 (exact for the powers of two that la_kv_write stores).
-//   e4m3: the hardware's conversion of pairs to fp16 (exact), fp32 products, one rounding.
-//   int8: with the low 7 bits L and the sign bit S of a code, p = 128 + L and q = 128 + 128 S by bit patterns of
-//         bf16, and p f - q f in one fused step (q f is exact).  q f overflows where f exceeds 2^118: the difference
-//         is taken first there.
-// Instructions on bits run at half rate, which bounds the conversion: per pair of codes these take two and a half to
-// three (moving e4m3's bits into bf16's places would take four).
+//   e4m3: the hardware's conversion of pairs to fp16 (exact).
+//   int8: the byte with its sign bit flipped, under the exponent of 2^10: 1152 plus the code in fp16.
+// Then fp32 products and one rounding.  Instructions on bits and conversions run at half rate, which bounds this: two and
+// a half a pair of codes before the two to fp32 (moving bits into bf16's places would take four and more).
 template <int FMT>
 __device__ __forceinline__ void convert16(const uint4 &w, float f, uint4 &o0, uint4 &o1) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -435,25 +433,11 @@ __device__ __forceinline__ void convert16(const uint4 &w, float f, uint4 &o0, ui
       v[k] = pack2(g.x * f, g.y * f);
     }
   } else {
-    const bool wide = f > 3.32306998946228968e35f;  // 2^118
-    const __nv_bfloat162 f2 = __float2bfloat162_rn(wide ? 1.f : f), nf = __float2bfloat162_rn(wide ? -1.f : -f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t b = __byte_perm(in[k >> 1], 0, k & 1 ? 0x4342 : 0x4140);
-      uint32_t p, q;
-      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(p) : "r"(b), "r"(0x007F007Fu), "r"(0x43004300u));
-      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q) : "r"(b), "r"(0x00800080u), "r"(0x43004300u));
-      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&p), f2,
-                                       __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&q), nf));
-      v[k] = *reinterpret_cast<const uint32_t *>(&r);
-    }
-    if (__any_sync(0xffffffffu, wide)) {
-      const __nv_bfloat162 g2 = __float2bfloat162_rn(wide ? f : 1.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v[k]), g2);
-        v[k] = *reinterpret_cast<const uint32_t *>(&r);
-      }
+      const uint32_t b = __byte_perm(in[k >> 1] ^ 0x80808080u, 0x64646464u, k & 1 ? 0x4342 : 0x4140);
+      const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+      v[k] = pack2((g.x - 1152.f) * f, (g.y - 1152.f) * f);
     }
   }
   o0 = make_uint4(v[0], v[1], v[2], v[3]);
@@ -550,8 +534,25 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         };
         int slot, nslot = 0;
         int pg = page_at(it.t0, slot), npg = -1;
+        // 8 bits: the scales of this lane's four keys (and values) of the tile after, by plain loads: as many bulk
+        // copies as there are boxes would cost more than the codes'
+        float4 nsk = make_float4(0.f, 0.f, 0.f, 0.f), nsv = nsk;
+        auto scales_at = [&](int t) {
+          const int64_t p = (int64_t)t * kTile + 4 * lane;
+          nsk = nsv = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p >= it.e.kv_end) return;
+          const uint32_t idx = (uint32_t)p / (uint32_t)a.page_size;
+          const int pg = a.table[(int64_t)it.e.seq * a.max_pages + idx];
+          if (pg < 0 || pg >= a.n_pages) return;
+          const int64_t at = ((int64_t)pg * a.Hkv + it.head) * a.page_size + (p - (int64_t)idx * a.page_size);
+          nsk = *reinterpret_cast<const float4 *>(a.ks + at);
+          nsv = *reinterpret_cast<const float4 *>(a.vs + at);
+        };
+        if (G::Q8) scales_at(it.t0);
         for (int i = 0; i < it.n && ok; ++i) {
           if (i + 1 < it.n) npg = page_at(it.t0 + i + 1, nslot);
+          const float4 sk = nsk, sv = nsv;
+          if (G::Q8 && i + 1 < it.n) scales_at(it.t0 + i + 1);
           // a missing page is read past the end of the page axis: zeros
           const int pc = pg >= 0 ? pg : (int)a.n_pages;
 #pragma unroll
@@ -571,19 +572,12 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             } else {
               const int s = seq % (G::NR > 0 ? G::NR : 1);
               if (!(ok = wait_on_warp(sy, G::B_REMPTY + s, ((seq / (G::NR > 0 ? G::NR : 1)) & 1) ^ 1, it.t0 + i))) break;
-              const uint32_t have = __popc(__ballot_sync(0xffffffffu, pg >= 0));
-              if (lane < nb && pg < 0)
-                for (int r = 0; r < a.box; ++r) sc[s * kTile + lane * a.box + r] = 0.f;
+              reinterpret_cast<float4 *>(sc + s * kTile)[lane] = kvi ? sv : sk;
               __syncwarp();
-              if (lane == 0) mbar_arrive_expect_tx(bars + G::B_RFULL + s, G::RAW + have * a.box * 4);
+              if (lane == 0) mbar_arrive_expect_tx(bars + G::B_RFULL + s, G::RAW);
               __syncwarp();
-              if (lane < nb) {
+              if (lane < nb)
                 tma_load_4d(raw_stage(s) + lane * a.box * D, tm, bars + G::B_RFULL + s, 0, it.head, slot, pc);
-                if (pg >= 0)
-                  bulk_load(sc + s * kTile + lane * a.box,
-                            (kvi ? a.vs : a.ks) + ((int64_t)pg * a.Hkv + it.head) * a.page_size + slot, a.box * 4,
-                            bars + G::B_RFULL + s);
-              }
             }
             if (i == 0 && kvi == 0) {  // the item's queries, after its first keys are on their way
               if (!(ok = wait_on_warp(sy, G::B_QEMPTY, (items & 1) ^ 1, it.t0))) {
