@@ -191,37 +191,56 @@ __device__ __forceinline__ void seq_span(const PaArgs &a, int64_t n, int64_t &st
   len = min(max((int64_t)a.cu[n + 1], start), a.T) - start;
 }
 
+// First entry of each sequence and first tile of each entry: searched in shared memory while there are at most
+// kPlanThreads of them (the usual call), else where they lie in the workspace.
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
-  __shared__ int64_t ws[32];
+  __shared__ int64_t ws[32], first_tile[kPlanThreads];
+  __shared__ int32_t first_entry[kPlanThreads];
   const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the main kernel's CTAs set themselves up meanwhile
   const int64_t per = a.per;
   int64_t sum, carry = 0;
-  for (int64_t n0 = 0; n0 < a.n_seqs; n0 += kPlanThreads) {
-    const int64_t n = n0 + tid;
-    int64_t st = 0, len = 0;
-    if (n < a.n_seqs) seq_span(a, n, st, len);
-    const int64_t k = (len + per - 1) / per;
-    const int64_t x = block_scan(k, ws, sum);
-    if (n < a.n_seqs) a.seq_ent[n + 1] = (int32_t)min(carry + x + k, (int64_t)a.e_max);
-    carry += sum;
+  const int64_t dense_k = (a.T + per - 1) / per;  // entries of a sequence of a dense batch
+  if (a.cu) {
+    for (int64_t n0 = 0; n0 < a.n_seqs; n0 += kPlanThreads) {
+      const int64_t n = n0 + tid;
+      int64_t st = 0, len = 0;
+      if (n < a.n_seqs) seq_span(a, n, st, len);
+      const int64_t k = (len + per - 1) / per;
+      const int64_t x = block_scan(k, ws, sum);
+      if (n < a.n_seqs) {
+        a.seq_ent[n + 1] = (int32_t)min(carry + x + k, (int64_t)a.e_max);
+        if (n0 == 0) first_entry[tid] = (int32_t)min(x, (int64_t)a.e_max);
+      }
+      carry += sum;
+    }
+    if (tid == 0) a.seq_ent[0] = 0;
+    __syncthreads();
+  } else {
+    carry = dense_k * a.n_seqs;
   }
-  if (tid == 0) a.seq_ent[0] = 0;
-  __syncthreads();
   // overlapping sequences (an invalid cu_seqlens) could ask for more entries than there is room for
   const int E = (int)min(carry, (int64_t)a.e_max);
+  const int32_t *se = a.n_seqs <= kPlanThreads ? first_entry : a.seq_ent;
   carry = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     const int e = e0 + tid;
     int64_t cnt = 0;
     if (e < E) {
-      int64_t lo = 0, hi = a.n_seqs;  // the last sequence whose first entry is <= e
-      while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (a.seq_ent[mid] <= e) lo = mid; else hi = mid;
+      int64_t lo = 0, t0;  // the last sequence whose first entry is <= e
+      if (a.cu) {
+        int64_t hi = a.n_seqs;
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) >> 1;
+          if (se[mid] <= e) lo = mid; else hi = mid;
+        }
+        t0 = (int64_t)(e - se[lo]) * per;
+      } else {
+        lo = e / dense_k;
+        t0 = (e - lo * dense_k) * per;
       }
       int64_t st, len;
       seq_span(a, lo, st, len);
-      const int64_t t0 = (int64_t)(e - a.seq_ent[lo]) * per;
       const int64_t kv = max((int64_t)a.kv_len[lo], (int64_t)0);
       Entry x;
       x.seq = (int)lo;
@@ -239,10 +258,14 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       a.ent[e] = x;
     }
     const int64_t x = block_scan(cnt, ws, sum);
-    if (e < E) a.pre[e] = carry + x;
+    if (e < E) {
+      a.pre[e] = carry + x;
+      if (e0 == 0) first_tile[tid] = x;
+    }
     carry += sum;
   }
   __syncthreads();
+  const int64_t *ft = E <= kPlanThreads ? first_tile : a.pre;
   const int64_t P = carry, W = P * a.Hkv;
   const int64_t parts = min((int64_t)a.G, W);  // none of them empty: parts are counted by their numbers
   for (int c = tid; c < a.G; c += kPlanThreads) {
@@ -253,15 +276,15 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
     w.count = s1 - s0;
     w.total = P;
     if (s1 > s0) {
-      const int64_t r = s0 % P;
+      w.head = (int)(s0 / P);
+      const int64_t r = s0 - w.head * P;
       int lo = 0, hi = E;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.pre[mid] <= r) lo = mid; else hi = mid;
+        if (ft[mid] <= r) lo = mid; else hi = mid;
       }
-      w.head = (int)(s0 / P);
       w.entry = lo;
-      w.off = (int)(r - a.pre[lo]);
+      w.off = (int)(r - ft[lo]);
     }
     a.work[c] = w;
     for (int i = 0; i < 8; ++i) a.arrived[8 * c + i] = 0;
@@ -507,6 +530,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan (and what came before it) is there
   auto op_slot = [&](int s) { return sm + G::OFF_OP + s * G::TILE; };
   auto raw_stage = [&](int s) { return sm + G::OFF_RAW + s * G::RAW; };
 
@@ -1353,8 +1377,17 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   if (e != cudaSuccess) return e;
   pa_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kern<<<a.G, G::THREADS, G::SMEM_BYTES, stream>>>(mq, mk, mv, a);
-  return cudaGetLastError();
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.G);
+  cfg.blockDim = dim3(G::THREADS);
+  cfg.dynamicSmemBytes = G::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a);
 }
 
 template <int D, int NQ>
