@@ -18,9 +18,10 @@
 //
 // Work.  The key tiles of all entries and heads stand in one row; CTA c of G (one
 // per SM) takes the c-th of G equal parts of it.  An entry cut by a border leaves
-// partial results (unnormalised o, m, l) in the workspace, and the warp that brings
-// the last part of a row joins them.  A small kernel lays out the row first:
-// lengths are known to the device only.
+// partial results (unnormalised o, m, l) in the workspace, which a last kernel joins
+// (joining inside, by whichever CTA came last, kept single CTAs busy for 12 us).  A
+// first one lays out the row: lengths are known to the device only.  Each kernel sets
+// itself up while the one before it ends.
 //
 // Roles (warps): 0 TMA producer (the tile's boxes on as many lanes; a box is a
 // power-of-two piece of a page), 1 MMA issuer (one thread), 2-3 values fix-up
@@ -146,8 +147,7 @@ struct PaArgs {
   Entry *ent;          // [e_max]
   int64_t *pre;        // [e_max + 1]
   CtaWork *work;       // [G]
-  uint32_t *arrived;   // [G][2][4]
-  float *po;           // [G][2][2][128][D]
+  float *po;           // [G][2][2][D / 4][128][4]: four columns of all rows side by side
   float2 *pml;         // [G][2][2][128]
 };
 
@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       w.off = (int)(r - ft[lo]);
     }
     a.work[c] = w;
-    for (int i = 0; i < 8; ++i) a.arrived[8 * c + i] = 0;
   }
   if (tid == 0) a.seq_ent[0] = E;  // the main kernel wraps to the next head after entry E - 1
 }
@@ -340,17 +339,6 @@ struct PaCfg {
                        R_CONV = NQ == 1 ? 48 : 64;
   static_assert(R_AUX <= R_LAUNCH && R_CONV <= R_LAUNCH && R_SOFT >= R_LAUNCH, "setmaxnreg .dec and .inc");
   static_assert(128 * R_AUX + 256 * R_SOFT + 32 * CONV * R_CONV <= THREADS * R_LAUNCH, "register split");
-};
-
-template <int V>
-struct Vec;
-template <>
-struct Vec<2> {
-  typedef float2 T;
-};
-template <>
-struct Vec<4> {
-  typedef float4 T;
 };
 
 // A piece of an entry: `n` key tiles from tile t0 on, of one cache head.
@@ -531,6 +519,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan (and what came before it) is there
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto op_slot = [&](int s) { return sm + G::OFF_OP + s * G::TILE; };
   auto raw_stage = [&](int s) { return sm + G::OFF_RAW + s * G::RAW; };
 
@@ -1088,7 +1077,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const int tile = two ? w : 0;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (it.first ? 1 : 0);
-      float *po = a.po + ((slot * 2 + tile) * kTile + r) * D;
+      float4 *po = reinterpret_cast<float4 *>(a.po) + (slot * 2 + tile) * (D / 4) * kTile + r;
       if (active) {
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -1138,9 +1127,9 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                                     pack2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
                                     pack2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
             } else {
-              float4 *dst = reinterpret_cast<float4 *>(po + 32 * q);
 #pragma unroll
-              for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              for (int u = 0; u < 8; ++u)
+                po[(8 * q + u) * kTile] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
             }
           }
         }
@@ -1153,73 +1142,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       }
       if (valid && whole && a.lse)
         a.lse[((int64_t)it.e.b * a.T + tok) * a.H + head] = (M + log2f(L)) * 0.6931471805599453f;
-      if (active && !whole) {
-        // leave the part, and join the entry's parts if this warp's rows are complete with it
-        if (valid) a.pml[(slot * 2 + tile) * kTile + r] = make_float2(M, L);
-        // tile s of the row of W tiles belongs to the last CTA c with floor(W c / parts) <= s
-        const int64_t total = a.work[blockIdx.x].total, W = total * a.Hkv, parts = a.work[blockIdx.x].parts;
-        const int64_t s0 = it.head * total + a.pre[it.entry], s1 = s0 + it.e.cnt - 1;
-        const int c0 = (int)(((s0 + 1) * parts - 1) / W), c1 = (int)(((s1 + 1) * parts - 1) / W);
-        __threadfence();
-        __syncwarp();
-        uint32_t before = 0;
-        if (lane == 0) before = atomicAdd(a.arrived + (c0 * 2 + tile) * 4 + quad, 1u);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == (uint32_t)(c1 - c0)) {
-          __threadfence();
-          // A lane keeps a row's statistics; eight rows at a time all lanes add up the parts, V columns each: as many
-          // loads are under way as registers hold.
-          constexpr int V = D / 32;
-          typedef typename Vec<V>::T VT;
-          const uint32_t rows_here = __ballot_sync(0xffffffffu, valid);
-          auto part_row = [&](int cc, int q) -> int64_t {
-            return ((2 * (int64_t)cc + (cc == c0 ? 1 : 0)) * 2 + tile) * kTile + quad * G::WROWS + q;
-          };
-          float mm = -INFINITY;
-#pragma unroll 8
-          for (int cc = c0; cc <= c1; ++cc) mm = fmaxf(mm, __ldcg(&a.pml[part_row(cc, lane)]).x);
-          const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 1
-          for (int r0 = 0; r0 < G::WROWS; r0 += 8) {
-            if (!((rows_here >> r0) & 0xFFu)) continue;
-            float acc[8][V], ls = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-              for (int u = 0; u < V; ++u) acc[k][u] = 0.f;
-#pragma unroll 2
-            for (int cc = c0; cc <= c1; ++cc) {
-              VT v[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const VT *>(a.po + part_row(cc, r0 + k) * D) + lane);
-              const float2 x = __ldcg(&a.pml[part_row(cc, lane)]);
-              const float wt = ex2(x.x - base);
-              ls = fmaf(wt, x.y, ls);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wt, r0 + k);
-#pragma unroll
-                for (int u = 0; u < V; ++u) acc[k][u] = fmaf(wk, reinterpret_cast<const float *>(&v[k])[u], acc[k][u]);
-              }
-            }
-            const float iv = ls == 0.f ? 0.f : 1.f / ls;
-            const float row_lse = (mm + log2f(ls)) * 0.6931471805599453f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float ik = __shfl_sync(0xffffffffu, iv, r0 + k);
-              const int row = quad * G::WROWS + r0 + k;
-              const int64_t rt = it.e.tok + (two ? w * a.tpt : 0) + row / a.g;
-              const int rh = it.head * a.g + row % a.g;
-              if (!((rows_here >> (r0 + k)) & 1u)) continue;
-              uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + (int64_t)it.e.b * a.o_sb +
-                                                           rt * a.o_st + (int64_t)rh * a.o_sh + V * lane);
-#pragma unroll
-              for (int u = 0; u < V / 2; ++u) dst[u] = pack2(acc[k][2 * u] * ik, acc[k][2 * u + 1] * ik);
-              if (a.lse && lane == r0 + k) a.lse[((int64_t)it.e.b * a.T + rt) * a.H + rh] = row_lse;
-            }
-          }
-        }
-      }
+      if (valid && !whole) a.pml[(slot * 2 + tile) * kTile + r] = make_float2(M, L);
       ++items;
     }
   } else if (G::Q8) {
@@ -1321,6 +1244,56 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
 }
 
+// ------------------------------------------------------------------ joining
+// Block c joins the entry that the border before CTA c cuts, if that is its first cut.  A thread takes eight columns of
+// a row; a warp's rows lie side by side.
+constexpr int kJoinThreads = 512;
+template <int D, int NQ>
+__global__ void __launch_bounds__(kJoinThreads) pa_join_kernel(const PaArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const CtaWork cw = a.work[c];
+  if (c == 0 || cw.count <= 0 || cw.off == 0) return;
+  const Entry e = a.ent[cw.entry];
+  // tile s of the row of W tiles belongs to the last CTA c with floor(W c / parts) <= s
+  const int64_t W = cw.total * a.Hkv, parts = cw.parts;
+  const int64_t s0 = cw.head * cw.total + a.pre[cw.entry], s1 = s0 + e.cnt - 1;
+  const int c0 = (int)(((s0 + 1) * parts - 1) / W), c1 = (int)(((s1 + 1) * parts - 1) / W);
+  if (c0 != c - 1) return;
+  constexpr int ROWS = NQ == 1 ? 64 : 128, CG = D / 8;
+  const bool two = NQ == 2 && e.ntok > a.tpt;
+  for (int task = threadIdx.x; task < (two ? 2 : 1) * ROWS * CG; task += kJoinThreads) {
+    const int r = task % ROWS, cg = (task / ROWS) % CG, tile = task / (ROWS * CG);
+    const int tk = tile * a.tpt + r / a.g;
+    if (r >= a.g * a.tpt || tk >= e.ntok) continue;
+    auto part = [&](int x) -> int64_t { return (2 * (int64_t)x + (x == c0 ? 1 : 0)) * 2 + tile; };
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int x = c0; x <= c1; ++x) m = fmaxf(m, a.pml[part(x) * kTile + r].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int x = c0; x <= c1; ++x) {
+      const int64_t at = part(x);
+      const float2 st = a.pml[at * kTile + r];
+      const float4 *src = reinterpret_cast<const float4 *>(a.po) + (at * (D / 4) + 2 * cg) * kTile + r;
+      const float4 u = src[0], v = src[kTile];
+      const float wt = ex2(st.x - base);
+      l = fmaf(wt, st.y, l);
+      o[0] = fmaf(wt, u.x, o[0]), o[1] = fmaf(wt, u.y, o[1]), o[2] = fmaf(wt, u.z, o[2]), o[3] = fmaf(wt, u.w, o[3]);
+      o[4] = fmaf(wt, v.x, o[4]), o[5] = fmaf(wt, v.y, o[5]), o[6] = fmaf(wt, v.z, o[6]), o[7] = fmaf(wt, v.w, o[7]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = e.tok + tk;
+    const int head = cw.head * a.g + r % a.g;
+    *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + (int64_t)e.b * a.o_sb + tok * a.o_st +
+                               (int64_t)head * a.o_sh + 8 * cg) =
+        make_uint4(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv), pack2(o[4] * inv, o[5] * inv),
+                   pack2(o[6] * inv, o[7] * inv));
+    if (a.lse && cg == 0) a.lse[((int64_t)e.b * a.T + tok) * a.H + head] = (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
 // ------------------------------------------------------------------ host side
 int tokens_per_tile(int g, int tiles) { return (tiles == 1 ? 64 : kTile) / g; }
 
@@ -1347,7 +1320,7 @@ int64_t max_entries(int64_t B, int64_t T, int64_t n_seqs, bool packed, int g) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-  size_t seq_ent, ent, pre, work, arrived, po, pml, bytes;
+  size_t seq_ent, ent, pre, work, po, pml, bytes;
 };
 Plan plan(int64_t e_max, int64_t n_seqs, int D, int G) {
   Plan p;
@@ -1361,7 +1334,6 @@ Plan plan(int64_t e_max, int64_t n_seqs, int D, int G) {
   p.ent = take((size_t)e_max * sizeof(Entry));
   p.pre = take((size_t)e_max * 8);
   p.work = take((size_t)G * sizeof(CtaWork));
-  p.arrived = take((size_t)G * 32);
   p.pml = take((size_t)G * 4 * kTile * 8);
   p.po = take((size_t)G * 4 * kTile * D * 4);
   p.bytes = at;
@@ -1387,7 +1359,10 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   cfg.stream = stream;
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a)) != cudaSuccess) return e;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, pa_join_kernel<D, NQ>, a);
 }
 
 template <int D, int NQ>
@@ -1458,7 +1433,6 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int G, void *workspace, cudaStre
   p.ent = (Entry *)(ws + pl.ent);
   p.pre = (int64_t *)(ws + pl.pre);
   p.work = (CtaWork *)(ws + pl.work);
-  p.arrived = (uint32_t *)(ws + pl.arrived);
   p.pml = (float2 *)(ws + pl.pml);
   p.po = (float *)(ws + pl.po);
 
