@@ -17,7 +17,7 @@
 // group's exponentials run beside the other group's products.
 //
 // Work.  The key tiles of all entries and heads stand in one row; CTA c of G (one
-// per SM) takes the c-th of G equal parts of it.  An entry cut by a border leaves
+// per SM) takes the c-th of G parts of equal cost of it.  An entry cut by a border leaves
 // partial results (unnormalised o, m, l) in the workspace, which a last kernel joins
 // (joining inside, by whichever CTA came last, kept single CTAs busy for 12 us).  A
 // first one lays out the row: lengths are known to the device only.  Each kernel sets
@@ -63,57 +63,37 @@ using tcsync::drain_bar;
 using tcsync::pack2;
 using tcsync::Sync;
 
-// Up to 64 probes of a barrier, in as few instructions as they take: many warps wait here beside few that work, on
-// the same issue slots (a probe returns after some hundred cycles, not after its suspend hint).
-__device__ __forceinline__ bool mbar_probe(uint64_t *bar, uint32_t parity) {
+// Bounded wait on a barrier: true once the phase has completed, false when the CTA has given up or this wait does (2^23
+// probes of some hundred cycles, a second or so), which is recorded.  It is kept short: it stands in some thirty
+// places, by warps that would share the instruction cache with the ones that work.
+__device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 16;\n"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
+      "mov.u32 n, 8388608;\n"
       "AGAIN:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\t"
       "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 p, n, 0;\n\t@p bra AGAIN;\n\t"
-      "setp.ne.u32 p, n, n;\n"
+      "setp.eq.u32 q, f, 0;\n\t"
+      "setp.ne.and.u32 q, n, 0, q;\n\t@q bra AGAIN;\n"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(smem_u32(sy.bar + idx)), "r"(parity), "r"(smem_u32(const_cast<int *>(sy.abort)))
       : "memory");
-  return ok != 0;
-}
-
-// tcsync::wait_bar by such probes; IDLE: by a warp that nobody waits for soon.
-template <bool IDLE = false>
-__device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile) {
-  uint64_t *b = sy.bar + idx;
-  if (mbar_test(b, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (IDLE) {
-      __nanosleep(200);
-      if (mbar_test(b, parity)) return true;
-    } else if (mbar_probe(b, parity)) {
-      return true;
-    }
-    if (*sy.abort) return false;
-    if (clock64() - t0 > tcsync::kTimeoutCycles) {
-      *sy.abort = 1;
-      atomicOr(sy.err, 1u);
-      atomicCAS(sy.where, 0u, 0x80000000u | ((uint32_t)(tile & 0x7FFFFF) << 8) | (uint32_t)idx);
-      return false;
-    }
+  if (!ok && !*sy.abort) {
+    *sy.abort = 1;
+    atomicOr(sy.err, 1u);
+    atomicCAS(sy.where, 0u, 0x80000000u | ((uint32_t)(tile & 0x7FFFFF) << 8) | (uint32_t)idx);
   }
+  return ok != 0;
 }
 __device__ __forceinline__ void arrive_n(uint64_t *bar, uint32_t n) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
-template <bool IDLE = false>
 __device__ __forceinline__ bool wait_on_warp(const Sync &sy, int idx, uint32_t parity, int tile) {
-  return __all_sync(0xffffffffu, wait_on<IDLE>(sy, idx, parity, tile));
+  return __all_sync(0xffffffffu, wait_on(sy, idx, parity, tile));
 }
 
 constexpr int kTile = 128;  // keys of a tile, rows of a query tile
@@ -124,10 +104,8 @@ struct alignas(16) Entry {
   int32_t pos, kv_end, lo, cnt;  // position of the first token; positions in reach; first key tile, key tiles
 };
 struct alignas(16) CtaWork {
-  int32_t head, entry, off;  // where this CTA's part starts: key tile `off` of an entry
-  int32_t parts;             // CTAs that have a part (every CTA the same)
-  int64_t count;             // key tiles
-  int64_t total;             // key tiles of one head (every CTA the same)
+  int32_t head, entry, off, pad;  // where this CTA's part starts: key tile `off` of an entry
+  int64_t start, count;           // that place in the row of tiles; key tiles
 };
 
 struct PaArgs {
@@ -145,7 +123,7 @@ struct PaArgs {
   int64_t s_page, s_tok, s_head;
   int32_t *seq_ent;    // [n_seqs + 1]
   Entry *ent;          // [e_max]
-  int64_t *pre;        // [e_max + 1]
+  int64_t *pre;        // [e_max][2]: cost and key tiles of the entries before
   CtaWork *work;       // [G]
   float *po;           // [G][2][2][D / 4][128][4]: four columns of all rows side by side
   float2 *pml;         // [G][2][2][128]
@@ -191,10 +169,17 @@ __device__ __forceinline__ void seq_span(const PaArgs &a, int64_t n, int64_t &st
   len = min(max((int64_t)a.cu[n + 1], start), a.T) - start;
 }
 
+// What a key tile and an entry cost a CTA, in thirds of a tile of two query tiles (about 2 us; one query tile: 1.4 us).
+// An entry costs about two tiles besides its own: its queries' way in, the first weights, its results.
+__device__ __forceinline__ int tile_cost(const PaArgs &a, const Entry &e) { return e.ntok > a.tpt ? 3 : 2; }
+__device__ __forceinline__ int64_t entry_cost(const PaArgs &a, const Entry &e) {
+  return (int64_t)tile_cost(a, e) * e.cnt + (e.ntok > a.tpt ? 6 : 3);
+}
+
 // First entry of each sequence and first tile of each entry: searched in shared memory while there are at most
 // kPlanThreads of them (the usual call), else where they lie in the workspace.
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
-  __shared__ int64_t ws[32], first_tile[kPlanThreads];
+  __shared__ int64_t ws[32], first_cost[kPlanThreads], begin[kPlanThreads + 1];
   __shared__ int32_t first_entry[kPlanThreads];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the main kernel's CTAs set themselves up meanwhile
@@ -223,9 +208,10 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
   const int E = (int)min(carry, (int64_t)a.e_max);
   const int32_t *se = a.n_seqs <= kPlanThreads ? first_entry : a.seq_ent;
   carry = 0;
+  int64_t tiles = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     const int e = e0 + tid;
-    int64_t cnt = 0;
+    int64_t cnt = 0, cost = 0;
     if (e < E) {
       int64_t lo = 0, t0;  // the last sequence whose first entry is <= e
       if (a.cu) {
@@ -256,38 +242,47 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       cnt = end > beg ? (end + kTile - 1) / kTile - x.lo : 1;  // nothing seen: one tile, all masked
       x.cnt = (int)cnt;
       a.ent[e] = x;
+      cost = entry_cost(a, x);
     }
-    const int64_t x = block_scan(cnt, ws, sum);
+    const int64_t t = block_scan(cnt, ws, sum);
+    if (e < E) a.pre[2 * (int64_t)e + 1] = tiles + t;
+    tiles += sum;
+    const int64_t x = block_scan(cost, ws, sum);
     if (e < E) {
-      a.pre[e] = carry + x;
-      if (e0 == 0) first_tile[tid] = x;
+      a.pre[2 * (int64_t)e] = carry + x;
+      if (e0 == 0) first_cost[tid] = x;
     }
     carry += sum;
   }
   __syncthreads();
-  const int64_t *ft = E <= kPlanThreads ? first_tile : a.pre;
-  const int64_t P = carry, W = P * a.Hkv;
-  const int64_t parts = min((int64_t)a.G, W);  // none of them empty: parts are counted by their numbers
-  for (int c = tid; c < a.G; c += kPlanThreads) {
-    const int64_t s0 = c < parts ? W * c / parts : 0, s1 = c < parts ? W * (c + 1) / parts : 0;
+  // Border c of G: where c G-ths of the cost are reached, at a tile (or an entry's start: what an entry costs besides its
+  // tiles comes first).  Its place in the row of tiles; a CTA between two equal borders has nothing.
+  const int64_t W = tiles * a.Hkv;
+  for (int c = tid; c <= a.G; c += kPlanThreads) {
     CtaWork w;
-    w.head = w.entry = w.off = 0;
-    w.parts = (int)parts;
-    w.count = s1 - s0;
-    w.total = P;
-    if (s1 > s0) {
-      w.head = (int)(s0 / P);
-      const int64_t r = s0 - w.head * P;
+    w.head = w.entry = w.off = w.pad = 0;
+    w.start = W;
+    w.count = 0;
+    if (c < a.G && E > 0) {
+      const int64_t s = carry * a.Hkv / a.G * c + carry * a.Hkv % a.G * c / a.G;
+      w.head = (int)(s / carry);
+      const int64_t r = s - w.head * carry;
       int lo = 0, hi = E;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (ft[mid] <= r) lo = mid; else hi = mid;
+        if ((E <= kPlanThreads ? first_cost[mid] : a.pre[2 * (int64_t)mid]) <= r) lo = mid; else hi = mid;
       }
+      const Entry x = a.ent[lo];
+      const int64_t in = r - a.pre[2 * (int64_t)lo] - entry_cost(a, x) + tile_cost(a, x) * (int64_t)x.cnt;
       w.entry = lo;
-      w.off = (int)(r - ft[lo]);
+      w.off = in > 0 ? (int)(in / tile_cost(a, x)) : 0;
+      w.start = w.head * tiles + a.pre[2 * (int64_t)lo + 1] + w.off;
     }
-    a.work[c] = w;
+    begin[c] = w.start;
+    if (c < a.G) a.work[c] = w;
   }
+  __syncthreads();
+  for (int c = tid; c < a.G; c += kPlanThreads) a.work[c].count = begin[c + 1] - begin[c];
   if (tid == 0) a.seq_ent[0] = E;  // the main kernel wraps to the next head after entry E - 1
 }
 
@@ -1039,9 +1034,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       const float mc = m;
       const bool mine = two || w == 0;
       if (!mine) {  // O[1] complete: the previous item's statistics have been read
-        if (!(ok = part_of ? wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0)
-                           : wait_on_warp<true>(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0)))
-          break;
+        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
         ++ocnt[1];
         if (lane < G::WROWS) ml[r] = make_float2(mc, l);
         __syncwarp();
@@ -1050,9 +1043,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         continue;
       }
       const bool join = !two;
-      if (!(ok = part_of ? wait_on_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0)
-                         : wait_on_warp<true>(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0)))
-        break;
+      if (!(ok = wait_on_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0))) break;
       ++ocnt[w];
       float M = mc, L = l, w0 = 1.f, w1 = 0.f;
       if (join) {
@@ -1100,10 +1091,10 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
               for (int j = rc.a; j < rc.d; ++j) {
                 if (j >= rc.b && j < rc.c) continue;
                 const int64_t p = (int64_t)t * kTile + j;
-                const int64_t idx = p / a.page_size;
+                const uint32_t idx = (uint32_t)p / (uint32_t)a.page_size;
                 const int pg = a.table[(int64_t)it.e.seq * a.max_pages + idx];
                 if (pg < 0 || pg >= a.n_pages || p < lo || p >= hi) continue;
-                const int sl = (int)(p % a.page_size);
+                const int sl = (int)((uint32_t)p - idx * (uint32_t)a.page_size);
                 const int64_t off = (int64_t)pg * a.s_page + (int64_t)sl * a.s_tok + (int64_t)it.head * a.s_head + 32 * q;
                 const float vs = G::Q8 ? a.vs[((int64_t)pg * a.Hkv + it.head) * a.page_size + sl] : 0.f;
                 if (FMT == LA_KV_INT8 && finite_f(vs)) continue;
@@ -1255,25 +1246,34 @@ __global__ void __launch_bounds__(kJoinThreads) pa_join_kernel(const PaArgs a) {
   const CtaWork cw = a.work[c];
   if (c == 0 || cw.count <= 0 || cw.off == 0) return;
   const Entry e = a.ent[cw.entry];
-  // tile s of the row of W tiles belongs to the last CTA c with floor(W c / parts) <= s
-  const int64_t W = cw.total * a.Hkv, parts = cw.parts;
-  const int64_t s0 = cw.head * cw.total + a.pre[cw.entry], s1 = s0 + e.cnt - 1;
-  const int c0 = (int)(((s0 + 1) * parts - 1) / W), c1 = (int)(((s1 + 1) * parts - 1) / W);
-  if (c0 != c - 1) return;
+  const int64_t t0 = cw.start - cw.off, t1 = t0 + e.cnt;  // the entry's tiles
+  __shared__ int parts[kPagedCtas], nparts;
+  if (threadIdx.x == 0) {
+    int n = 0, x = c - 1;
+    while (x > 0 && a.work[x].count == 0) --x;
+    if (a.work[x].start <= t0) {  // else cut before
+      parts[n++] = x;
+      for (x = c; x < a.G && a.work[x].start < t1; ++x)
+        if (a.work[x].count > 0) parts[n++] = x;
+    }
+    nparts = n;
+  }
+  __syncthreads();
+  if (nparts == 0) return;
   constexpr int ROWS = NQ == 1 ? 64 : 128, CG = D / 8;
   const bool two = NQ == 2 && e.ntok > a.tpt;
   for (int task = threadIdx.x; task < (two ? 2 : 1) * ROWS * CG; task += kJoinThreads) {
     const int r = task % ROWS, cg = (task / ROWS) % CG, tile = task / (ROWS * CG);
     const int tk = tile * a.tpt + r / a.g;
     if (r >= a.g * a.tpt || tk >= e.ntok) continue;
-    auto part = [&](int x) -> int64_t { return (2 * (int64_t)x + (x == c0 ? 1 : 0)) * 2 + tile; };
+    auto part = [&](int x) -> int64_t { return (2 * (int64_t)parts[x] + (x == 0 ? 1 : 0)) * 2 + tile; };
     float m = -INFINITY;
 #pragma unroll 8
-    for (int x = c0; x <= c1; ++x) m = fmaxf(m, a.pml[part(x) * kTile + r].x);
+    for (int x = 0; x < nparts; ++x) m = fmaxf(m, a.pml[part(x) * kTile + r].x);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int x = c0; x <= c1; ++x) {
+    for (int x = 0; x < nparts; ++x) {
       const int64_t at = part(x);
       const float2 st = a.pml[at * kTile + r];
       const float4 *src = reinterpret_cast<const float4 *>(a.po) + (at * (D / 4) + 2 * cg) * kTile + r;
@@ -1332,7 +1332,7 @@ Plan plan(int64_t e_max, int64_t n_seqs, int D, int G) {
   };
   p.seq_ent = take((size_t)(n_seqs + 1) * 4);
   p.ent = take((size_t)e_max * sizeof(Entry));
-  p.pre = take((size_t)e_max * 8);
+  p.pre = take((size_t)e_max * 16);
   p.work = take((size_t)G * sizeof(CtaWork));
   p.pml = take((size_t)G * 4 * kTile * 8);
   p.po = take((size_t)G * 4 * kTile * D * 4);
