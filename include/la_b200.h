@@ -623,23 +623,24 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  *   workspace   device scratch of at least la_paged_attn_workspace_size(...)
  *               bytes (NULL allowed when that is 0), 256-byte aligned; need not be
  *               initialised.  Calls whose work may overlap on the GPU (two streams,
- *               two captured graphs) need a workspace each.
- * Slots that no query of the call sees may hold anything, NaN included, with
- * one exception: in a LA_KV_BF16 cache the values (v) at positions below
- * kv_len[n] must be finite where a query of the sequence does not see them but
- * sees another position of the same 128.  A position that a query does see takes
- * part as the formula says, infinities and NaN too.
+ *               two captured graphs) need a workspace each.  About 40 MB at D = 128
+ *               (results of keys split over CTAs) plus 48 bytes for every 64
+ *               rows of queries.
+ * A position that a query does not see has no part in its result whatever it
+ * holds, infinities and NaN included; slots that no query of the call sees may
+ * be uninitialised.  A position that it does see takes part as the formula
+ * says, infinities and NaN too.  out must not overlap q, the cache or lse.
  * Reads of the cache follow 64-bit offsets; page_table, kv_len and cu_seqlens
  * are read on the device only and their values are never trusted with an
  * address: no value of theirs makes the call read or write out of bounds.
  *
  * Kernels: bf16 with D 64 or 128, page_size a multiple of 8, at most 128 query
  * heads a cache head and q strides that are not zero run on the tensor cores;
- * every other shape, f32 and LA_FLAG_SIMT on the CUDA cores, in fp32.
- * la_paged_attn_path tells (as la_fwd_chunk_path does; -1: rejected).
+ * every other shape, f32 and LA_FLAG_SIMT on the CUDA cores, in fp32 (tens of times
+ * slower).  la_paged_attn_path tells (as la_fwd_chunk_path does; -1: rejected).
  *
- * Arithmetic: 8-bit rows enter as the bf16 values they stand for (a scale that
- * is not a power of two is rounded to bf16 first on the tensor cores); scores,
+ * Arithmetic: 8-bit rows enter as the values they stand for, on the tensor cores
+ * rounded to bf16 (which changes nothing where scales are powers of two); scores,
  * softmax statistics and outputs are accumulated in fp32; on the tensor cores the
  * softmax weights are rounded to bf16 for the product with v; out is rounded once.
  * Results do not depend on other sequences of the call beyond fp32 rounding: where
@@ -697,8 +698,9 @@ LA_API la_status la_fwd_chunk_noalloc(const la_tensor *q, const la_tensor *k, co
  * wait that runs out makes the CTA give up, drain its asynchronous copies, free
  * its tensor memory and return, and records the failure here instead of
  * hanging or trapping.
- *   flags   receives a bit set: 1 = a wait timed out, 2 = draining timed out
- *           (0 = no failure since the last reset)
+ *   flags   receives a bit set: 1 = a wait timed out, 2 = draining timed out,
+ *           4 = la_paged_attn found its shared memory misaligned (0 = no failure
+ *           since the last reset)
  *   detail  receives the first failed wait: bit 31 set, chunk index << 8,
  *           barrier index in the low 8 bits (0 if none)
  *   reset   nonzero: clear both words after reading

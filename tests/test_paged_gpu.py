@@ -445,3 +445,73 @@ def test_several_items_and_cut_ones_a_cta(la, lens, ctx, H, Hkv, D, page, window
     c = Case(lens, ctx, H, Hkv, D, page, fmt, seed=len(lens) + D, layout="head" if D == 64 else "token")
     hold(c, *attn(la, c, c.fill(la, "cuda"), window=window), window=window)
     assert la.device_error(reset=True) == (0, 0)
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_more_sequences_than_the_plan_takes_at_once(la, packed):
+    """1500 sequences: the plan's searches leave shared memory.  Every tenth is empty in the packed batch."""
+    n = 1500
+    lens = [0 if packed and i % 10 == 3 else 1 + (i % 3 if packed else 0) for i in range(n)]
+    c = Case(lens, [(7 * i) % 150 for i in range(n)], 2, 2, 64, 16, I8, seed=30)
+    k, v, ks, vs = c.fill(la, "cuda")
+    q, cu = (c.q[None], c.cu.cuda()) if packed else (c.q[:, None], None)
+    out, lse = la.la_paged_attn(q.cuda(), k, v, c.table.cuda(), torch.tensor(c.kv_len, dtype=torch.int32, device="cuda"),
+                                cu_seqlens=cu, k_scale=ks, v_scale=vs, return_lse=True)
+    hold(c, out, lse)
+
+
+@pytest.mark.parametrize("H,D,lens", [(65, 64, [3, 1]), (100, 128, [2]), (128, 64, [1, 5]), (33, 64, [4])])
+def test_many_heads_on_one_cache_head(la, H, D, lens):
+    """Groups of heads that leave rows of a query tile unused, or more of them than a 64-row tile holds."""
+    c = Case(lens, [300] * len(lens), H, 1, D, 16, BF, seed=H)
+    hold(c, *attn(la, c, c.fill(la, "cuda")))
+
+
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("fmt", [BF, E4])
+def test_values_that_are_not_numbers_element_by_element(la, fmt, window, simt):
+    """An infinity (bf16) or a NaN code (e4m3) in one element of a value row reaches that column of the queries
+    that see the row, and nothing else: 200 queries over two key tiles, rows seen by some of a query tile."""
+    c = Case([200], [60], 4, 2, 64, 16, fmt, seed=14)
+    k, v, ks, vs = c.fill(la, "cuda")
+    clean = attn(la, c, (k, v, ks, vs), window=window, simt=simt)[0][0].cpu()
+    for p, h, d in ((150, 0, 7), (250, 1, 63), (61, 0, 32)):
+        row = v[c.table[0, p // 16], p % 16, h]
+        (row.view(torch.int8) if fmt == E4 else row)[d] = 0x7F if fmt == E4 else -math.inf
+    out = attn(la, c, (k, v, ks, vs), window=window, simt=simt)[0][0].cpu()
+    want = clean.clone()
+    for p, h, d in ((150, 0, 7), (250, 1, 63), (61, 0, 32)):
+        for i in range(200):
+            if p <= 60 + i and (not window or p > 60 + i - window):
+                want[i, 2 * h:2 * h + 2, d] = math.nan if fmt == E4 else -math.inf
+    bad = ~torch.isfinite(want)
+    assert torch.equal(torch.isfinite(out), ~bad)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+def test_scales_of_every_size_and_other_ones(la):
+    """Rows whose scales reach from 2^-100 to 2^100 in one cache, and scales that are not powers of two (rounded to
+    the nearest bf16 product)."""
+    for fmt in (E4, I8):
+        c = Case([3], [200], 2, 2, 64, 16, fmt, seed=19)
+        c.v_rows[0] = (c.v_rows[0].double() * torch.exp2(torch.randint(-100, 100, (203, 1, 1)).double())).to(BF)
+        hold(c, *attn(la, c, c.fill(la, "cuda")))
+        c = Case([3], [200], 2, 2, 64, 16, fmt, seed=20)
+        k, v, ks, vs = c.fill(la, "cuda")
+        ks *= 1.25  # 5 significant bits with e4m3's codes: exact; int8's round to bf16
+        stored = c.stored(0)
+        c.stored = lambda n: [(stored[0] * 1.25).to(torch.float32).to(BF).double(), stored[1]]
+        hold(c, *attn(la, c, (k, v, ks, vs)))
+
+
+def test_a_workspace_may_hold_anything_and_is_checked(la):
+    c = Case([1, 70], [3000, 100], 8, 2, 128, 16, E4, seed=23)
+    cache = c.fill(la, "cuda")
+    need = la.paged_attn_workspace_size(1, 71, 8, 128, 2, True, 2, 16, E4)
+    for byte in (0, 0xFF, 0x7F):
+        ws = torch.full((need,), byte, dtype=torch.uint8, device="cuda")
+        hold(c, *attn(la, c, cache, workspace=ws))
+    with pytest.raises(la.LaError):
+        attn(la, c, cache, workspace=ws[: need - 1])
