@@ -132,31 +132,29 @@ struct PaArgs {
 // ------------------------------------------------------------------ schedule
 constexpr int kPlanThreads = 1024;
 
-// Exclusive prefix of v over the block, plus the block's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t &sum) {
+// Exclusive prefixes of u and v over the block, and its sums.
+struct Pair {
+  int64_t u, v;
+};
+__device__ __forceinline__ Pair block_scan(Pair x, Pair *warp_sums, Pair &sum) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int64_t s = warp_sums[lane];
+  auto warp_scan = [&](Pair p) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+      const int64_t a = __shfl_up_sync(0xffffffffu, p.u, o), b = __shfl_up_sync(0xffffffffu, p.v, o);
+      if (lane >= o) p.u += a, p.v += b;
     }
-    warp_sums[lane] = s;
-  }
+    return p;
+  };
+  const Pair p = warp_scan(x);
+  if (lane == 31) warp_sums[w] = p;
   __syncthreads();
-  const int64_t before = w ? warp_sums[w - 1] : 0;
+  if (w == 0) warp_sums[lane] = warp_scan(warp_sums[lane]);
+  __syncthreads();
+  const Pair before = w ? warp_sums[w - 1] : Pair{0, 0};
   sum = warp_sums[31];
   __syncthreads();
-  return before + x - v;
+  return Pair{before.u + p.u - x.u, before.v + p.v - x.v};
 }
 
 __device__ __forceinline__ void seq_span(const PaArgs &a, int64_t n, int64_t &start, int64_t &len) {
@@ -179,12 +177,14 @@ __device__ __forceinline__ int64_t entry_cost(const PaArgs &a, const Entry &e) {
 // First entry of each sequence and first tile of each entry: searched in shared memory while there are at most
 // kPlanThreads of them (the usual call), else where they lie in the workspace.
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
-  __shared__ int64_t ws[32], first_cost[kPlanThreads], begin[kPlanThreads + 1];
+  __shared__ Pair ws[32];
+  __shared__ int64_t first_cost[kPlanThreads], begin[kPlanThreads + 1];
   __shared__ int32_t first_entry[kPlanThreads];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the main kernel's CTAs set themselves up meanwhile
   const int64_t per = a.per;
-  int64_t sum, carry = 0;
+  Pair sum;
+  int64_t carry = 0;
   const int64_t dense_k = (a.T + per - 1) / per;  // entries of a sequence of a dense batch
   if (a.cu) {
     for (int64_t n0 = 0; n0 < a.n_seqs; n0 += kPlanThreads) {
@@ -192,12 +192,12 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       int64_t st = 0, len = 0;
       if (n < a.n_seqs) seq_span(a, n, st, len);
       const int64_t k = (len + per - 1) / per;
-      const int64_t x = block_scan(k, ws, sum);
+      const int64_t x = block_scan(Pair{k, 0}, ws, sum).u;
       if (n < a.n_seqs) {
         a.seq_ent[n + 1] = (int32_t)min(carry + x + k, (int64_t)a.e_max);
         if (n0 == 0) first_entry[tid] = (int32_t)min(x, (int64_t)a.e_max);
       }
-      carry += sum;
+      carry += sum.u;
     }
     if (tid == 0) a.seq_ent[0] = 0;
     __syncthreads();
@@ -244,15 +244,14 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const PaArgs a) {
       a.ent[e] = x;
       cost = entry_cost(a, x);
     }
-    const int64_t t = block_scan(cnt, ws, sum);
-    if (e < E) a.pre[2 * (int64_t)e + 1] = tiles + t;
-    tiles += sum;
-    const int64_t x = block_scan(cost, ws, sum);
+    const Pair x = block_scan(Pair{cost, cnt}, ws, sum);
     if (e < E) {
-      a.pre[2 * (int64_t)e] = carry + x;
-      if (e0 == 0) first_cost[tid] = x;
+      a.pre[2 * (int64_t)e] = carry + x.u;
+      a.pre[2 * (int64_t)e + 1] = tiles + x.v;
+      if (e0 == 0) first_cost[tid] = x.u;
     }
-    carry += sum;
+    carry += sum.u;
+    tiles += sum.v;
   }
   __syncthreads();
   // Border c of G: where c G-ths of the cost are reached, at a tile (or an entry's start: what an entry costs besides its
@@ -1236,33 +1235,37 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
 }
 
 // ------------------------------------------------------------------ joining
-// Block c joins the entry that the border before CTA c cuts, if that is its first cut.  A thread takes eight columns of
-// a row; a warp's rows lie side by side.
+// Blocks (c, .) join the entry that the border before CTA c cuts, if that is its first cut.  A thread takes eight
+// columns of a row; a warp's rows lie side by side.
 constexpr int kJoinThreads = 512;
+static_assert(kPagedCtas <= kJoinThreads, "a thread looks a part up");
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) pa_join_kernel(const PaArgs a) {
+  __shared__ int parts[kJoinThreads], members[kJoinThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const CtaWork cw = a.work[c];
   if (c == 0 || cw.count <= 0 || cw.off == 0) return;
   const Entry e = a.ent[cw.entry];
   const int64_t t0 = cw.start - cw.off, t1 = t0 + e.cnt;  // the entry's tiles
-  __shared__ int parts[kPagedCtas], nparts;
-  if (threadIdx.x == 0) {
-    int n = 0, x = c - 1;
-    while (x > 0 && a.work[x].count == 0) --x;
-    if (a.work[x].start <= t0) {  // else cut before
-      parts[n++] = x;
-      for (x = c; x < a.G && a.work[x].start < t1; ++x)
-        if (a.work[x].count > 0) parts[n++] = x;
-    }
-    nparts = n;
-  }
+  CtaWork x;
+  x.count = 0;
+  if (tid < a.G) x = a.work[tid];
+  const bool in = x.count > 0 && x.start < t1 && x.start + x.count > t0;
+  const uint32_t mask = __ballot_sync(0xffffffffu, in);
+  if ((tid & 31) == 0) members[tid >> 5] = __popc(mask);
   __syncthreads();
-  if (nparts == 0) return;
+  int rank = __popc(mask & ((1u << (tid & 31)) - 1)), nparts = 0;
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < tid >> 5) rank += members[i];
+    nparts += members[i];
+  }
+  if (in) parts[rank] = tid;
+  __syncthreads();
+  if (parts[1] != c) return;  // cut before
   constexpr int ROWS = NQ == 1 ? 64 : 128, CG = D / 8;
   const bool two = NQ == 2 && e.ntok > a.tpt;
-  for (int task = threadIdx.x; task < (two ? 2 : 1) * ROWS * CG; task += kJoinThreads) {
+  for (int task = blockIdx.y * kJoinThreads + tid; task < (two ? 2 : 1) * ROWS * CG; task += gridDim.y * kJoinThreads) {
     const int r = task % ROWS, cg = (task / ROWS) % CG, tile = task / (ROWS * CG);
     const int tk = tile * a.tpt + r / a.g;
     if (r >= a.g * a.tpt || tk >= e.ntok) continue;
@@ -1360,6 +1363,7 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.G, NQ * (NQ == 1 ? 64 : 128) * (D / 8) / kJoinThreads);  // a task a thread
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, pa_join_kernel<D, NQ>, a);
