@@ -63,14 +63,14 @@ using tcsync::drain_bar;
 using tcsync::pack2;
 using tcsync::Sync;
 
-// Bounded wait on a barrier: true once the phase has completed, false when the CTA has given up or this wait does (2^23
-// probes of some hundred cycles, a second or so), which is recorded.  It is kept short: it stands in some thirty
-// places, by warps that would share the instruction cache with the ones that work.
+// Bounded wait on a barrier: true once the phase has completed, false when the CTA has given up or this wait does (2^19
+// probes; one that fails sleeps for 7800 cycles: about two seconds), which is recorded.  It is kept short: it stands in
+// some thirty places, by warps that would share the instruction cache with the ones that work.
 __device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
-      "mov.u32 n, 8388608;\n"
+      "mov.u32 n, 524288;\n"
       "AGAIN:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
       "ld.volatile.shared.u32 f, [%3];\n\t"
