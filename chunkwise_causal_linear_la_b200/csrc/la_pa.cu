@@ -377,7 +377,7 @@ struct Walk {
 __device__ __forceinline__ void sees(const PaArgs &a, const Entry &e, int tk, int &lo, int &hi) {
   const int p = e.pos + tk;
   hi = min(p + 1, e.kv_end);
-  lo = a.window > 0 ? max(0, p - (a.window - 1)) : 0;
+  lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;  // (p may be far below 0, the window near 2^31)
 }
 
 // Of the keys of tile t: all tokens of the entry see those in [b, c); some those in
@@ -818,7 +818,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         int x, lo1, hi0, y;
         sees(a, it.e, 0, x, hi0);
         sees(a, it.e, max(it.e.ntok, 1) - 1, lo1, y);
-        full0 = (lo1 + kTile - 1) / kTile - it.t0;
+        full0 = (int)(((uint32_t)lo1 + kTile - 1) / kTile) - it.t0;
         full1 = max(hi0, 0) / kTile - it.t0;
       }
       float m = -INFINITY, l = 0.f;  // the maximum in powers of two: scale log2(e) times the score

@@ -181,6 +181,15 @@ def test_windows(la, window, simt):
     hold(c, *attn(la, c, cache, window=window, simt=simt), window=window, simt=simt)
 
 
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("fmt", [BF, I8])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31, 2 ** 40])
+def test_windows_past_every_position(la, window, fmt, simt):
+    """The widest windows hide nothing, from queries before position 0 either."""
+    c = Case([60, 3], [-20, 200], 4, 2, 64, 16, fmt, seed=31)
+    hold(c, *attn(la, c, c.fill(la, "cuda"), window=window, simt=simt), window=window, simt=simt)
+
+
 @pytest.mark.parametrize("fmt", [BF, E4])
 @pytest.mark.parametrize("H,D,page", [(4, 16, 16), (4, 32, 5), (2, 256, 16), (4, 128, 20)])
 def test_shapes_off_the_tensor_cores(la, H, D, page, fmt):
