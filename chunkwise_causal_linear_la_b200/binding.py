@@ -723,7 +723,7 @@ def paged_attn_workspace_size(B, T, H, D, n_seqs, varlen, H_kv, page_size, cache
                               dtype=torch.bfloat16, flags=0) -> int:
     """Bytes of workspace la_paged_attn needs (0: none)."""
     n = load_library().la_paged_attn_workspace_size(B, T, H, D, n_seqs, int(bool(varlen)), H_kv, page_size,
-                                                    _KV[cache_dtype], _DT[dtype], flags)
+                                                    _KV.get(cache_dtype, -1), _DT.get(dtype, -1), flags)
     if n == ctypes.c_size_t(-1).value:
         raise LaError(LA_ERR_INVALID_ARG, "la_paged_attn_workspace_size rejected the arguments")
     return int(n)
@@ -731,7 +731,8 @@ def paged_attn_workspace_size(B, T, H, D, n_seqs, varlen, H_kv, page_size, cache
 
 def paged_attn_path(H, D, H_kv, page_size, cache_dtype=torch.bfloat16, dtype=torch.bfloat16, flags=LA_FLAG_NONE) -> int:
     """Kernel la_paged_attn runs for this shape: LA_PATH_TENSOR_CORE, LA_PATH_CUDA_CORE, or -1."""
-    return int(load_library().la_paged_attn_path(H, D, H_kv, page_size, _KV[cache_dtype], _DT[dtype], flags))
+    return int(load_library().la_paged_attn_path(H, D, H_kv, page_size, _KV.get(cache_dtype, -1), _DT.get(dtype, -1),
+                                                 flags))
 
 
 def la_paged_attn(q, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_scale=None, v_scale=None, scale=None,
@@ -747,6 +748,8 @@ def la_paged_attn(q, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_sc
     tl, tc = _index("kv_len", kv_len, (n,)), _index("cu_seqlens", cu_seqlens, (n + 1,))
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 [B, T, H] tensor")
+    if workspace is not None and not workspace.is_contiguous():  # a broadcast one has fewer bytes than elements
+        raise TypeError("workspace must be contiguous")
     dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, cu_seqlens, out, lse, workspace)
     need = lib.la_paged_attn_workspace_size(B, T, H, D, n, tc is not None, cache.H, cache.page_size, cache.format,
                                             tq.dtype, flags)
@@ -759,7 +762,7 @@ def la_paged_attn(q, k_cache, v_cache, page_table, kv_len, cu_seqlens=None, k_sc
             lse = q.new_empty((B, T, H), dtype=torch.float32)
         if need and workspace is None:
             workspace = q.new_empty(need, dtype=torch.uint8)
-    st = lib.la_paged_attn(tq, cache, table, max_pages, tl, tc, n, D ** -0.5 if scale is None else scale, window,
+    st = lib.la_paged_attn(tq, cache, table, max_pages, tl, tc, n, max(D, 1) ** -0.5 if scale is None else scale, window,
                            _describe(out), None if lse is None else lse.data_ptr(), flags,
                            None if workspace is None else workspace.data_ptr(),
                            0 if workspace is None else workspace.numel() * workspace.element_size(),

@@ -140,12 +140,15 @@ def test_paths_and_workspace(lib):
             assert b.paged_attn_path(H, D, Hkv, page, fmt) == b.LA_PATH_TENSOR_CORE
     with pytest.raises(b.LaError):
         b.paged_attn_workspace_size(1, 64, 15, 128, 1, False, 4, 16)
-    # entries (32 bytes and an 8-byte prefix each) grow with the batch, the parts of 148 CTAs do not
+    assert b.paged_attn_path(16, 64, 4, 16, torch.uint8) == -1 == b.paged_attn_path(16, 64, 4, 16, dtype=torch.float16)
+    with pytest.raises(b.LaError):
+        b.paged_attn_workspace_size(1, 64, 16, 128, 1, False, 4, 16, torch.float16)
+    # entries (32 bytes and two 8-byte prefixes each) grow with the batch, the parts of 148 CTAs do not
     small = b.paged_attn_workspace_size(1, 1, 16, 128, 1, False, 4, 16)
     assert small >= 148 * 4 * 128 * (128 + 2) * 4
     assert b.paged_attn_workspace_size(1, 1, 16, 64, 1, False, 4, 16) < small
     many = b.paged_attn_workspace_size(1, 1 << 20, 16, 128, 1000, True, 4, 16)
-    assert many - small >= ((1 << 20) // 64 + 1000 - 1) * 40
+    assert many - small >= ((1 << 20) // 64 + 1000 - 1) * 48
     assert b.paged_attn_workspace_size(1, 0, 16, 128, 1, False, 4, 16) == 0
 
 
@@ -166,6 +169,8 @@ def test_binding_refuses_what_it_cannot_describe():
     table, kl = torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
     with pytest.raises(TypeError):  # an 8-bit cache without scales
         b.la_paged_attn(q, k, k, table, kl)
+    with pytest.raises(TypeError):  # a workspace with fewer bytes than elements
+        b.la_paged_attn(q, k, k, table, kl, k_scale=s, v_scale=s, workspace=torch.zeros(1).expand(1 << 26))
     with pytest.raises(TypeError):  # scales of another layout
         b.la_paged_attn(q, k, k, table, kl, k_scale=s.transpose(1, 2), v_scale=s)
     with pytest.raises(TypeError):
