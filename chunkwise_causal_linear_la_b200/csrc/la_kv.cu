@@ -11,7 +11,11 @@
 // Both kernels move every byte once and are bound by memory: D / 8 threads share a
 // row, each with 16 bytes of its dense side, keys and values of one row in one
 // thread so that two loads are in flight, and the row's maximum goes through
-// shuffles.
+// shuffles.  Measured for 16 sequences of up to 16384 tokens, 8 heads of 128, against
+// the rate of a plain copy: bf16 written 203 us (94%), read 206 us (93%); e4m3 216 us
+// (67%), 179 us (81%); int8 215 us (67%), 172 us (84%).  The 8-bit forms are held
+// by their instructions (two thirds of the issue slots; conversions at half rate and
+// less) beside memory.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -240,7 +244,8 @@ __global__ void __launch_bounds__(kKvThreads, 8) kv_read_kernel(const KvMoveArgs
   }
 }
 
-// Eight turns a block where that still leaves eight blocks an SM, else one.
+// Eight turns a block where that still leaves eight blocks an SM, else one: a block's look-ups are a chain of loads
+// (with one turn large calls reach 55% of the copy rate, with eight 67 - 94%), and small calls need all SMs.
 template <template <typename, int> class K>
 cudaError_t launch(const KvMoveArgs &a, cudaStream_t stream) {
   const int64_t rows = a.B * a.T * a.c.H;

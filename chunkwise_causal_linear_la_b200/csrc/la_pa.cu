@@ -9,12 +9,12 @@
 // two runs over disjoint keys join by their weights 2^(m_a - m), 2^(m_b - m).
 //
 // Rows.  The g query heads that share a cache head are rows of one product: row
-// r of a 128-row tile is token r / g, head r % g of floor(128 / g) tokens.  An entry
-// of work is one or two such tiles of a sequence and one cache head.  With two
+// r of a tile of 128 (or 64) is token r / g, head r % g of floor(128 / g) tokens.  An
+// entry of work is one or two such tiles of a sequence and one cache head.  With two
 // tiles the two softmax warpgroups take a tile each over the same keys; with one
-// (single tokens, short chunks, the end of a prompt) they take the even and the odd
-// key tiles of it, with an accumulator each, joined at the end.  Either way one
-// group's exponentials run beside the other group's products.
+// (single tokens, short chunks, the end of a prompt) they take the first and the
+// second half of each key tile, with an accumulator each, joined at the end.  Either
+// way one group's exponentials run beside the other group's products.
 //
 // Work.  The key tiles of all entries and heads stand in one row; CTA c of G (one
 // per SM) takes the c-th of G parts of equal cost of it.  An entry cut by a border leaves
@@ -24,22 +24,31 @@
 // itself up while the one before it ends.
 //
 // Roles (warps): 0 TMA producer (the tile's boxes on as many lanes; a box is a
-// power-of-two piece of a page), 1 MMA issuer (one thread), 2-3 values fix-up
-// (bf16), 4-7 and 8-11 softmax, 12-15 conversion (8-bit caches: codes become bf16
-// operands, exact for power-of-two scales).
-//   QK:  S[w] = Q K^T     (M = 128, N = 128 keys, K = D)        S in TMEM
-//   PV:  O[w] += P V      (M = 128, N = D, K = 128 keys)        P (bf16) over S in TMEM
-// Tensor-core instructions of one thread run in order, so PV(i) has read P before
-// QK(i + 2) overwrites it, and the commit that announces S(i + 2) also says that O
-// holds PV(i): the softmax group may rescale O then without another barrier.
+// power-of-two piece of a page), 1 MMA issuer, 2-3 values fix-up (bf16), 4-7 and 8-11
+// softmax, from 12 on conversion (8-bit caches: codes become bf16 operands, exact for
+// power-of-two scales).
+//   QK:  S[w] = Q K^T     (M = 128 or 64, N = 128 keys, K = D)   S in TMEM
+//   PV:  O[w] += P V      (N = D, K = 128 keys; 64 a group)      P (bf16) over S in TMEM
+// Tensor-core instructions of one thread run in order, so the product that reads P is
+// done before the next scores overwrite it.  With two tiles the commit that announces
+// S[w] of the next key tile also says that O[w] holds the one before; where a group
+// has to rescale O between the halves of a tile, or with one query tile (whose
+// scores run two key tiles ahead), it waits for the product itself.
 //
 // What a query does not see must not reach it even where it is an infinity or a NaN:
 // scores are masked by selection, but 0 * inf in PV would be NaN.  Rows that no query
 // of the entry sees are zeroed; in rows that some see, values that are not finite
 // are taken out of the operand and added at the end for the queries that see them.
 //
-// Every wait is bounded (la_tc_sync.cuh): on a timeout the CTA records it, drains and
-// returns.
+// Every wait is bounded: on a timeout the CTA records it, drains and returns.
+//
+// What bounds it, measured on one B200 (bf16 unless said, 8 cache heads of 128):
+//   2048 tokens over 16384, 32 heads     254 us, 1.01 PFLOP/s (61% of the library's matrix product): a softmax group's
+//                                        chain (scores in, exponentials, P out) beside its products; tensor pipe 54%
+//   256 single tokens over up to 8192    342 us, 6.3 TB/s (97% of a copy): memory
+//   one token over 1,048,576, e4m3       369 us, 3.0 TB/s: conversion of codes, 1100 cycles for the keys or the values
+//                                        of a tile, of which the instructions' issue is 530
+//   44 tokens and 4 pieces, e4m3         197 us: a new entry costs a CTA 4 - 6 us beside its key tiles
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -1157,7 +1166,8 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       if (lane == 0) bad[(items & 15) * 16 + cw] = 0;
       __syncwarp();
       // Even shares beside two full softmax groups.  When the rows are few all of the softmax runs on the first quarter
-      // of the SM (the first rows belong to its warps): the conversion warps there take an eighth together.
+      // of the SM (the first rows belong to its warps): the conversion warps there take an eighth together.  (Even
+      // shares for few rows too: no slower in pages of 64, slower in pages of 16, where the producer lives there too.)
       const bool even = D == 64 || it.e.ntok * a.g > G::WROWS;
       const int first = even ? ci * (TURNS / SET) : ((SET == 8 ? 0xDB917520u : 0xC720u) >> (4 * ci)) & 15;
       const int last = first + (even ? TURNS / SET : ((SET == 8 ? 0x32212231u : 0x4552u) >> (4 * ci)) & 15);
@@ -1308,7 +1318,8 @@ int box_rows(int64_t page_size) {  // largest power of two that divides the page
 
 // Query tiles of an entry: one of 64 rows where the sequences have no more rows each on average (single tokens, drafts:
 // the two softmax groups take half of each key tile, and shared memory goes to more of those), else two of 128 (they
-// share the keys).
+// share the keys).  Measured with 64 rows and with 128 for single tokens: 256 over up to 8192 (bf16) 344 and 469 us.
+// Prompts need the shared keys: a CTA that reads 64 rows' worth of keys does a quarter of the products for them.
 int query_tiles(int64_t B, int64_t T, int64_t n_seqs, bool packed, int g) {
   const int64_t tokens = packed ? T : B * T;
   return g <= 64 && tokens <= n_seqs * tokens_per_tile(g, 1) ? 1 : 2;

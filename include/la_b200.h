@@ -624,8 +624,9 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  *               bytes (NULL allowed when that is 0), 256-byte aligned; need not be
  *               initialised.  Calls whose work may overlap on the GPU (two streams,
  *               two captured graphs) need a workspace each.  About 40 MB at D = 128
- *               (results of keys split over CTAs) plus 48 bytes for every 64
- *               rows of queries.
+ *               (results of keys split over CTAs) plus 52 bytes for every
+ *               sequence and 48 for every 64 rows (tokens times query heads of a
+ *               cache head).
  * A position that a query does not see has no part in its result whatever it
  * holds, infinities and NaN included; slots that no query of the call sees may
  * be uninitialised.  A position that it does see takes part as the formula
