@@ -24,9 +24,9 @@
 // itself up while the one before it ends.
 //
 // Roles (warps): 0 TMA producer (the tile's boxes on as many lanes; a box is a
-// power-of-two piece of a page), 1 MMA issuer, 2-3 values fix-up (bf16), 4-7 and 8-11
-// softmax, from 12 on conversion (8-bit caches: codes become bf16 operands, exact for
-// power-of-two scales).
+// power-of-two piece of a page), 1 MMA issuer, 2-3 values fix-up (bf16) or scales
+// (8-bit caches, one query tile), 4-7 and 8-11 softmax, from 12 on conversion (8-bit
+// caches: codes become bf16 operands, exact for power-of-two scales).
 //   QK:  S[w] = Q K^T     (M = 128 or 64, N = 128 keys, K = D)   S in TMEM
 //   PV:  O[w] += P V      (N = D, K = 128 keys; 64 a group)      P (bf16) over S in TMEM
 // Tensor-core instructions of one thread run in order, so the product that reads P is
@@ -46,8 +46,8 @@
 //   2048 tokens over 16384, 32 heads     254 us, 1.01 PFLOP/s (61% of the library's matrix product): a softmax group's
 //                                        chain (scores in, exponentials, P out) beside its products; tensor pipe 54%
 //   256 single tokens over up to 8192    342 us, 6.3 TB/s (97% of a copy): memory
-//   one token over 1,048,576, e4m3       369 us, 3.0 TB/s: conversion of codes, 1100 cycles for the keys or the values
-//                                        of a tile, of which the instructions' issue is 530
+//   one token over 1,048,576, e4m3       357 us, 3.1 TB/s: conversion of codes (244 us without it, 240 without the
+//                                        softmax's work too; its instructions alone would take 1060 of 2980 cycles a tile)
 //   44 tokens and 4 pieces, e4m3         197 us: a new entry costs a CTA 4 - 6 us beside its key tiles
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -300,6 +300,10 @@ struct PaCfg {
   static constexpr bool Q8 = FMT != LA_KV_BF16;
   static constexpr int CONV = Q8 ? (NQ == 1 ? 16 : 8) : 0;  // conversion warps
   static constexpr int THREADS = 384 + 32 * CONV;
+  // With one query tile and 8-bit codes a tile is short beside the issuing warp's waits and commits: what ends together is
+  // announced together (scores with the keys' slot, a product with the values'), P with the values, and scales have
+  // warps of their own (one token over 1M, e4m3: 369 -> 357 us).
+  static constexpr bool LEAN = Q8 && NQ == 1;
   static constexpr int ROWS = NQ == 1 ? 64 : 128;    // rows of a query tile
   static constexpr int WROWS = ROWS / 4;             // of them, a softmax warp's
   static constexpr int SLABS = D / 64;               // 64-column slabs of a bf16 tile
@@ -499,8 +503,9 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   if (tid == 0) {
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t cnt = 1;
-      if (G::Q8 && i < G::NS) cnt = G::CONV / 2;                        // FULL: conversion warps
+      if (G::Q8 && i < G::NS) cnt = G::CONV / 2 + (G::LEAN && (i & 1) ? 8 : 0);  // FULL: conversion (and softmax) warps
       if (!G::Q8 && i >= G::B_EMPTY && i < G::B_EMPTY + G::NS) cnt = 3;  // products done, seen by the fix-up warps
+      if (i >= G::B_RFULL && i < G::B_RFULL + G::NR) cnt = G::LEAN ? 2 : 1;  // codes on their way, scales there
       if (i >= G::B_REMPTY && i < G::B_REMPTY + G::NR) cnt = G::CONV / 2;  // codes read
       if (i >= G::B_PFULL && i < G::B_PFULL + 2) cnt = 4;               // softmax warps
       if (i >= G::B_OEMPTY && i < G::B_OEMPTY + 2) cnt = 4;
@@ -564,11 +569,11 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           nsk = *reinterpret_cast<const float4 *>(a.ks + at);
           nsv = *reinterpret_cast<const float4 *>(a.vs + at);
         };
-        if (G::Q8) scales_at(it.t0);
+        if (G::Q8 && !G::LEAN) scales_at(it.t0);
         for (int i = 0; i < it.n && ok; ++i) {
           if (i + 1 < it.n) npg = page_at(it.t0 + i + 1, nslot);
           const float4 sk = nsk, sv = nsv;
-          if (G::Q8 && i + 1 < it.n) scales_at(it.t0 + i + 1);
+          if (G::Q8 && !G::LEAN && i + 1 < it.n) scales_at(it.t0 + i + 1);
           // a missing page is read past the end of the page axis: zeros
           const int pc = pg >= 0 ? pg : (int)a.n_pages;
 #pragma unroll
@@ -588,7 +593,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             } else {
               const int s = seq % (G::NR > 0 ? G::NR : 1);
               if (!(ok = wait_on_warp(sy, G::B_REMPTY + s, ((seq / (G::NR > 0 ? G::NR : 1)) & 1) ^ 1, it.t0 + i))) break;
-              reinterpret_cast<float4 *>(sc + s * kTile)[lane] = kvi ? sv : sk;
+              if (!G::LEAN) reinterpret_cast<float4 *>(sc + s * kTile)[lane] = kvi ? sv : sk;
               __syncwarp();
               if (lane == 0) mbar_arrive_expect_tx(bars + G::B_RFULL + s, G::RAW);
               __syncwarp();
@@ -643,7 +648,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           for (int kk = 0; kk < D / 16; ++kk)
             umma_bf16(tbase + G::T_S + w * kTile, dq + (((kk >> 2) * G::QSLAB + (kk & 3) * 32) >> 4),
                       dk + (((kk >> 2) * G::SLAB + (kk & 3) * 32) >> 4), ID_QK, kk > 0);
-          umma_commit(bars + G::B_SFULL + w);
+          if (!G::LEAN) umma_commit(bars + G::B_SFULL + w);
         }
         __syncwarp();
       };
@@ -727,7 +732,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             const uint32_t vs = (seq + 2 * i + 1) % G::NS;
             if (!(ok = values(i))) break;
             if (i == 0 && !(ok = o_free(0) && o_free(1))) break;
-            if (!(ok = wait_on_warp(sy, G::B_PSPLIT + b, bcnt[b] & 1, it.t0 + i))) break;
+            if (!G::LEAN && !(ok = wait_on_warp(sy, G::B_PSPLIT + b, bcnt[b] & 1, it.t0 + i))) break;
             ++bcnt[b];
             tc_fence_after();
             const uint64_t dv = dv0 + (uint64_t)(vs * (G::TILE >> 4));
@@ -738,7 +743,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                              dv + ((kk * 2048) >> 4), ID_PV, (i > 0 || (kk & 3) > 0) ? 1u : 0u);
             }
             __syncwarp();
-            commit(G::B_ODONE);
+            if (!G::LEAN) commit(G::B_ODONE);
             commit(G::B_EMPTY + vs);
             if (i + 1 == it.n) {
               commit(G::B_OFULL);
@@ -752,6 +757,39 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       commit(G::B_DRAIN);  // products under way end before tensor memory is freed
       drain_bar(sy, G::B_DRAIN, 0);
       __syncwarp();
+    } else if (G::LEAN) {
+      // -------------------------------------------------------------- scales: of keys (warp 2) and values (warp 3)
+      // (With two query tiles the producer does this.  With one it would be late with the codes: 64 sequences up to
+      // 16384 in int8, pages of 16, 141 us so and 126 with warps of their own; two query tiles, mixed batch, 197 and 230.)
+      constexpr int NRr = G::NR > 0 ? G::NR : 1;
+      const int kvi = warp - 2;
+      const float *from = kvi ? a.vs : a.ks;
+      int rs = kvi;
+      uint32_t rph = 1;
+      bool ok = true;
+      while (ok && walk.next(a, it)) {
+        auto scales_at = [&](int i) -> float4 {
+          const int64_t p = (int64_t)(it.t0 + i) * kTile + 4 * lane;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i >= it.n || p >= it.e.kv_end) return x;
+          const uint32_t idx = (uint32_t)p / (uint32_t)a.page_size;
+          const int pg = a.table[(int64_t)it.e.seq * a.max_pages + idx];
+          if (pg >= 0 && pg < a.n_pages)
+            x = *reinterpret_cast<const float4 *>(from + ((int64_t)pg * a.Hkv + it.head) * a.page_size +
+                                                  ((uint32_t)p - idx * (uint32_t)a.page_size));
+          return x;
+        };
+        float4 next = scales_at(0);
+        for (int i = 0; i < it.n; ++i) {
+          const float4 x = next;
+          next = scales_at(i + 1);
+          if (!(ok = wait_on_warp(sy, G::B_REMPTY + rs, rph, it.t0 + i))) break;
+          reinterpret_cast<float4 *>(sc + rs * kTile)[lane] = x;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + G::B_RFULL + rs);
+          if ((rs += 2) >= NRr) rs = kvi, rph ^= 1;
+        }
+      }
     } else if (!G::Q8) {
       // -------------------------------------------------------------- values fix-up
       // These warps see every tile and take part in its release: a slot is not filled again before they have
@@ -941,7 +979,9 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         }
         for (int i = 0; i < it.n && part_of; ++i, ++dcnt) {
           const int b = i & 1;
-          if (!(ok = wait_on_warp(sy, G::B_SFULL + b, scnt[b] & 1, it.t0 + i))) break;
+          const uint32_t seq = 2 * dcnt;  // (LEAN) this tile's keys in the ring of slots; its values come next
+          if (!(ok = G::LEAN ? wait_on_warp(sy, G::B_EMPTY + seq % G::NS, (seq / G::NS) & 1, it.t0 + i)
+                             : wait_on_warp(sy, G::B_SFULL + b, scnt[b] & 1, it.t0 + i))) break;
           ++scnt[b];
           if (active) {
             tc_fence_after();
@@ -998,7 +1038,8 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   hl[x][y] *= f[y];
                 }
                 if (i > 0) {  // O must hold the tile before
-                  if (!wait_on_warp(sy, G::B_ODONE, (dcnt - 1) & 1, it.t0 + i)) {
+                  if (!(G::LEAN ? wait_on_warp(sy, G::B_EMPTY + (seq - 1) % G::NS, ((seq - 1) / G::NS) & 1, it.t0 + i)
+                                : wait_on_warp(sy, G::B_ODONE, (dcnt - 1) & 1, it.t0 + i))) {
                     ok = false;
                     break;
                   }
@@ -1023,7 +1064,8 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             tc_fence_before();
           }
           __syncwarp();
-          if (lane == 0) arrive_n(bars + G::B_PSPLIT + b, quad == 0 ? 1 + idle : 1);
+          if (lane == 0)
+            arrive_n(bars + (G::LEAN ? G::B_FULL + (seq + 1) % G::NS : G::B_PSPLIT + b), quad == 0 ? 1 + idle : 1);
           if (!ok) break;
         }
         // statistics of row `lane`
