@@ -43,8 +43,9 @@
 // Every wait is bounded: on a timeout the CTA records it, drains and returns.
 //
 // What bounds it, measured on one B200 (bf16 unless said, 8 cache heads of 128):
-//   2048 tokens over 16384, 32 heads     254 us (275 back to back, at the power limit), 1.01 PFLOP/s (61% of the library's matrix product): a softmax group's
-//                                        chain (scores in, exponentials, P out) beside its products; tensor pipe 54%
+//   2048 tokens over 16384, 32 heads     254 us (275 back to back, at the power limit), 1.01 PFLOP/s (61% of the
+//                                        library's matrix product): a softmax group's chain (scores in, exponentials,
+//                                        P out) beside its products; tensor pipe 54%
 //   256 single tokens over up to 8192    342 us (356 back to back), 6.3 TB/s (97% of a copy): memory
 //   one token over 1,048,576, e4m3       357 us, 3.1 TB/s: conversion of codes (244 us without it, 240 without the
 //                                        softmax's work too; its instructions alone would take 1060 of 2980 cycles a tile)
