@@ -628,9 +628,10 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  *               sequence and 48 for every 64 rows (tokens times query heads of a
  *               cache head).
  * A position that a query does not see has no part in its result whatever it
- * holds, infinities and NaN included; slots that no query of the call sees may
- * be uninitialised.  A position that it does see takes part as the formula
- * says, infinities and NaN too.  out must not overlap q, the cache or lse.
+ * holds, infinities and NaN included, codes whose product with their scale is
+ * infinite too; slots that no query of the call sees may be uninitialised.  A
+ * position that it does see takes part as the formula says, infinities and NaN
+ * too.  out must not overlap q, the cache or lse.
  * Reads of the cache follow 64-bit offsets; page_table, kv_len and cu_seqlens
  * are read on the device only and their values are never trusted with an
  * address: no value of theirs makes the call read or write out of bounds.

@@ -1,0 +1,62 @@
+"""Paged cache and the attention over it at the ends of the number ranges, and what repeated calls return."""
+import math
+
+import pytest
+import torch
+
+from paged_util import Case
+
+pytestmark = pytest.mark.gpu
+E4, I8, BF = torch.float8_e4m3fn, torch.int8, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def la():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import chunkwise_causal_linear_la_b200 as la
+
+    la.load_library()
+    return la
+
+
+def attn(la, c, cache, **kw):
+    dev = torch.device("cuda")
+    k, v, ks, vs = cache
+    return la.la_paged_attn(c.q.to(dev)[None], k, v, c.table.to(dev),
+                            torch.tensor(c.kv_len, dtype=torch.int32, device=dev), cu_seqlens=c.cu.to(dev),
+                            k_scale=ks, v_scale=vs, return_lse=True, **kw)
+
+
+# ------------------------------------------- values whose code times scale leaves the range
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("window", [0, 7])
+@pytest.mark.parametrize("L,D", [(9, 64), (9, 128), (40, 64), (40, 128), (200, 128)])
+@pytest.mark.parametrize("fmt", [E4, I8])
+def test_values_past_the_range_reach_only_the_queries_that_see_them(la, fmt, L, D, window, simt):
+    """Rows of values under a finite scale whose products with some codes are infinite: a query that does not see
+    such a row returns what it returns without it, and one that does gets an infinity of the code's sign where the
+    product is one.  Entries of one query tile (9 tokens) and of two."""
+    c = Case([L], [100], 4, 2, D, 16, fmt, seed=L + D)
+    k, v, ks, vs = c.fill(la, "cuda")
+    flags = la.LA_FLAG_SIMT if simt else 0
+    clean = attn(la, c, (k, v, ks, vs), window=window, flags=flags)[0][0].cpu()
+    spots = [(104, 0), (107, 1)] + ([(250, 0)] if L > 150 else [])
+    past = {}
+    for p, h in spots:
+        pg, sl = int(c.table[0, p // 16]), p % 16
+        vs[pg, h, sl] = 2.0 ** 125
+        code = v[pg, sl, h].float().cpu()
+        past[p, h] = torch.sign(code) * (code.abs() >= 8)  # 8 * 2^125 = 2^128
+        assert int((past[p, h] != 0).sum()) > 0
+    out = attn(la, c, (k, v, ks, vs), window=window, flags=flags)[0][0].cpu()
+    for i in range(L):
+        at = 100 + i
+        for h in range(2):
+            seen = [past[p, g] for p, g in spots if g == h and p <= at and (not window or p > at - window)]
+            o = out[i, 2 * h:2 * h + 2]
+            if not seen:
+                assert torch.equal(o, clean[i, 2 * h:2 * h + 2]), (i, h)
+            elif not simt and len(seen) == 1:  # (in fp32, as the CUDA cores hold values, a weight times 2^133 may be finite)
+                for d in torch.nonzero(seen[0]).flatten().tolist():
+                    assert bool((o[:, d] == seen[0][d] * math.inf).all()), (i, h, d)
