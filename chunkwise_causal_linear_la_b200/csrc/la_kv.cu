@@ -96,6 +96,18 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
   return make_uint2(w[0], w[1]);
 }
 
+// Rows whose max |x| rounds to a code whose value is 2^128, beyond fp32 (from 248 2^120 on, and above 127 2^121; in bits),
+// have the scale 2^kTopExp: there e4m3's 256 becomes 240, int8's 64 becomes 63.
+template <int FMT>
+constexpr uint32_t kTopBits = FMT == LA_KV_E4M3 ? 0x7F780000u : 0x7F7E0001u;
+template <int FMT>
+constexpr int kTopExp = FMT == LA_KV_E4M3 ? 120 : 122;
+template <int FMT>
+__device__ __forceinline__ uint32_t keep_in_range(uint32_t w) {
+  if (FMT == LA_KV_E4M3) return w - (__vcmpeq4(w & 0x7F7F7F7Fu, 0x78787878u) & 0x01010101u);
+  return __vmins4(__vmaxs4(w, 0xC1C1C1C1u /* -63 */), 0x3F3F3F3Fu);
+}
+
 // Where a token of the batch stands.  A block's threads look its few tokens up once (a search among the sequences and
 // a table entry, each a chain of loads) and leave them in shared memory for its rows.
 struct Place {
@@ -201,13 +213,22 @@ __global__ void __launch_bounds__(kKvThreads, 8) kv_write_kernel(const KvMoveArg
     if (p.live) {
 #pragma unroll
       for (int kvi = 0; kvi < 2; ++kvi) {
-        const bool finite = m[kvi] < 0x7F800000u;
-        const int e = finite ? scale_exp<FMT>(m[kvi]) : 0;
-        const uint2 code = finite ? encode8<FMT>(x[kvi], __uint_as_float((uint32_t)(127 - e) << 23)) : make_uint2(0, 0);
+        uint2 code;
+        float scale;
+        if (m[kvi] < kTopBits<FMT>) {
+          const int e = scale_exp<FMT>(m[kvi]);
+          code = encode8<FMT>(x[kvi], __uint_as_float((uint32_t)(127 - e) << 23));
+          scale = __uint_as_float((uint32_t)(127 + e) << 23);
+        } else if (m[kvi] < 0x7F800000u) {
+          code = encode8<FMT>(x[kvi], __uint_as_float((uint32_t)(127 - kTopExp<FMT>) << 23));
+          code = make_uint2(keep_in_range<FMT>(code.x), keep_in_range<FMT>(code.y));
+          scale = __uint_as_float((uint32_t)(127 + kTopExp<FMT>) << 23);
+        } else {  // an infinity or a NaN in the row
+          code = make_uint2(0, 0);
+          scale = __uint_as_float(0x7FC00000u);
+        }
         *reinterpret_cast<uint2 *>((kvi ? a.c.v : a.c.k) + p.off + 8 * part) = code;
-        if (part == 0)
-          (kvi ? a.c.vs : a.c.ks)[p.scale] =
-              finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+        if (part == 0) (kvi ? a.c.vs : a.c.ks)[p.scale] = scale;
       }
     }
   }

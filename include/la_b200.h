@@ -541,8 +541,10 @@ LA_API la_status la_bwd_chunk_gated_norm(const la_tensor *q, const la_tensor *k,
  * formats keep one scale per row, a power of two, so that code * scale is exact
  * in bf16: s = 2^e, the smallest with max |x| <= qmax s and e >= -126, and
  * code = x / s rounded to nearest even (qmax 448 for e4m3, 127 for int8; e4m3
- * without infinities, as NVIDIA and OCP define it).  A row that holds an
- * infinity or a NaN gets a NaN scale and codes of zero: it reads back as NaN. */
+ * without infinities, as NVIDIA and OCP define it); a code whose product with s
+ * would be 2^128 (rows above 1.93 2^127) is the next one towards zero, so that
+ * finite rows read back finite.  A row that holds an infinity or a NaN gets a NaN
+ * scale and codes of zero: it reads back as NaN. */
 typedef enum { LA_KV_BF16 = 0, LA_KV_E4M3 = 1, LA_KV_INT8 = 2 } la_kv_format;
 
 /*

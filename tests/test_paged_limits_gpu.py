@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from paged_util import Case
+from paged_util import Case, quantise
 
 pytestmark = pytest.mark.gpu
 E4, I8, BF = torch.float8_e4m3fn, torch.int8, torch.bfloat16
@@ -60,3 +60,40 @@ def test_values_past_the_range_reach_only_the_queries_that_see_them(la, fmt, L, 
             elif not simt and len(seen) == 1:  # (in fp32, as the CUDA cores hold values, a weight times 2^133 may be finite)
                 for d in torch.nonzero(seen[0]).flatten().tolist():
                     assert bool((o[:, d] == seen[0][d] * math.inf).all()), (i, h, d)
+
+
+# ------------------------------------------------------------- the largest finite rows
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("fmt", [E4, I8])
+def test_the_largest_rows_read_back_finite(la, fmt, dtype):
+    """Rows up to the type's largest number: codes and scales of keys and of values are the formula's, but for a code whose
+    product with the scale would be infinite, which is one step of the grid nearer to zero."""
+    dev = torch.device("cuda")
+    top = torch.finfo(dtype).max
+    gen = torch.Generator().manual_seed(5)
+    x = (torch.rand((2, 1, 12, 2, 64), generator=gen, dtype=torch.float64) * 2 - 1) * top
+    x[:, 0, 1] = top
+    x[:, 0, 2] = -top
+    x[:, 0, 3] = top * (248 / 256)           # half way between e4m3's 240 and 256: to even is up
+    x[:, 0, 4] = 63.5 * 2.0 ** 122           # half way between int8's 63 and 64
+    x[:, 0, 5] = 127.0 * 2.0 ** 120
+    x[:, 0, 6] = 0
+    x[0, 0, 7, :, ::3] = -top                # keys and values have rows of their own
+    x[1, 0, 8, :, ::3] = top
+    x = x.to(dtype)
+    k, v, ks, vs = la.kv_cache(1, 16, 2, 64, fmt)
+    table, kl = torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.tensor([12], dtype=torch.int32, device=dev)
+    la.la_kv_write(x[0].to(dev), x[1].to(dev), k, v, table, kl, k_scale=ks, v_scale=vs)
+    changed = 0
+    for cache, scale, rows in ((k, ks, x[0, 0]), (v, vs, x[1, 0])):
+        code, s = quantise(rows.double(), fmt)
+        over = (code * s).abs() >= 2.0 ** 128
+        changed += int(over.sum())
+        code = torch.where(over, code.sign() * (240.0 if fmt == E4 else 63.0), code)
+        assert torch.equal(scale[0, :, :12].T.cpu().double(), s[..., 0])
+        assert torch.equal(cache[0, :12].float().cpu().double(), code)
+        assert bool(((code * s - rows.double()).abs() <= 2.0 ** -4 * rows.double().abs() + s).all())
+    assert changed > 200
+    for odt in (BF, torch.float32):
+        for r in la.la_kv_read(k, v, table, 12, k_scale=ks, v_scale=vs, dtype=odt):
+            assert bool(torch.isfinite(r).all())
