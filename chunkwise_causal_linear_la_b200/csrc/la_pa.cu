@@ -394,6 +394,12 @@ __device__ __forceinline__ void sees(const PaArgs &a, const Entry &e, int tk, in
   lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;  // (p may be far below 0, the window near 2^31)
 }
 
+// What the sum of weighted values is multiplied with.  The largest weight is 1 or more, so a sum of zero means a row that
+// sees nothing (zeros), or one whose scores are all -infinity (NaN, the formula's 0 / 0).
+__device__ __forceinline__ float factor(float l, bool sees_any) {
+  return l != 0.f ? 1.f / l : sees_any ? __uint_as_float(0x7FC00000u) : 0.f;
+}
+
 // Of the keys of tile t: all tokens of the entry see those in [b, c); some those in
 // [a, d); none the rest (tile-relative, clamped).
 struct Reach {
@@ -1119,7 +1125,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       for (int x = 0; x < (G::Q8 ? G::CONV : 2); ++x) any_bad |= bad[(items & 15) * 16 + x];
       const int64_t tok = it.e.tok + tk;
       const int head = it.head * a.g + r % a.g;
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = factor(L, lo < hi);
       const int tile = two ? w : 0;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (it.first ? 1 : 0);
       float4 *po = reinterpret_cast<float4 *>(a.po) + (slot * 2 + tile) * (D / 4) * kTile + r;
@@ -1353,7 +1359,9 @@ __global__ void __launch_bounds__(kJoinThreads) pa_join_kernel(const PaArgs a) {
       o[0] = fmaf(wt, u.x, o[0]), o[1] = fmaf(wt, u.y, o[1]), o[2] = fmaf(wt, u.z, o[2]), o[3] = fmaf(wt, u.w, o[3]);
       o[4] = fmaf(wt, v.x, o[4]), o[5] = fmaf(wt, v.y, o[5]), o[6] = fmaf(wt, v.z, o[6]), o[7] = fmaf(wt, v.w, o[7]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    int lo, hi;
+    sees(a, e, tk, lo, hi);
+    const float inv = factor(l, lo < hi);
     const int64_t tok = e.tok + tk;
     const int head = cw.head * a.g + r % a.g;
     *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + (int64_t)e.b * a.o_sb + tok * a.o_st +

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_simt_kernel(const PagedArgs
   for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
     float x = 0.f;
     for (int w = 0; w < kWarps; ++w) x = fmaf(wt[w], so[w][d], x);
-    out[d] = from_f32<T>(Ls == 0.f ? 0.f : x / Ls);  // nothing seen: zeros
+    out[d] = from_f32<T>(j1 > j0 ? x / Ls : 0.f);  // nothing seen: zeros; all scores -infinity: 0 / 0
   }
   if (a.lse && threadIdx.x == 0) a.lse[t * a.H + h] = M + logf(Ls);
 }

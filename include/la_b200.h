@@ -633,7 +633,8 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  * holds, infinities and NaN included, codes whose product with their scale is
  * infinite too; slots that no query of the call sees may be uninitialised.  A
  * position that it does see takes part as the formula says, infinities and NaN
- * too.  out must not overlap q, the cache or lse.
+ * too: a query whose scores are all -infinity gets NaN (0 / 0) and an lse of
+ * -infinity.  out must not overlap q, the cache or lse.
  * Reads of the cache follow 64-bit offsets; page_table, kv_len and cu_seqlens
  * are read on the device only and their values are never trusted with an
  * address: no value of theirs makes the call read or write out of bounds.

@@ -97,3 +97,20 @@ def test_the_largest_rows_read_back_finite(la, fmt, dtype):
     for odt in (BF, torch.float32):
         for r in la.la_kv_read(k, v, table, 12, k_scale=ks, v_scale=vs, dtype=odt):
             assert bool(torch.isfinite(r).all())
+
+
+# ----------------------------------------------------------- scores that are all -infinity
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("L,ctx", [(1, 20), (9, 100), (70, 300), (1, 20000)])
+def test_scores_that_are_all_minus_infinity(la, L, ctx, simt):
+    """Keys of +infinity in one element, under a query of -1 there: every score it sees is -infinity, the sum of the
+    weights is 0, and the output is the formula's 0 / 0; its log-sum-exp is -infinity.  Queries of +1 there give NaN for
+    both.  A query before position 0 still gives zeros.  One entry, two query tiles, keys split over CTAs."""
+    c = Case([L, 3], [ctx, -2], 4, 2, 64, 16, BF, seed=L)
+    c.k_rows[0][:, :, 5] = math.inf
+    c.q[:L, :2, 5], c.q[:L, 2:, 5] = -1.0, 1.0
+    out, lse = attn(la, c, c.fill(la, "cuda"), flags=la.LA_FLAG_SIMT if simt else 0)
+    assert bool(torch.isnan(out[0, :L]).all())
+    assert bool((lse[0, :L, :2] == -math.inf).all()) and bool(torch.isnan(lse[0, :L, 2:]).all())
+    assert bool((out[0, L:L + 2] == 0).all()) and bool((lse[0, L:L + 2] == -math.inf).all())
+    assert bool(torch.isfinite(out[0, L + 2:]).all()) and bool(torch.isfinite(lse[0, L + 2:]).all())
