@@ -217,7 +217,9 @@ la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int3
   if (cache->D != q->D) return fail(LA_ERR_INVALID_ARG, "the cache has another head dim");
   if (q->H % cache->H) return fail(LA_ERR_INVALID_ARG, "the query heads are not a multiple of the cache's heads");
   if ((s = check_seqs(q, cu_seqlens, n_seqs)) != LA_OK) return s;
-  if (!(scale > 0.f) || !isfinite(scale)) return fail(LA_ERR_INVALID_ARG, "scale must be positive and finite");
+  // the kernels weigh by powers of two: the scale times log2(e) has to be a number too
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f))
+    return fail(LA_ERR_INVALID_ARG, "scale must be positive and at most 2.35e38");
   if (window < 0) return fail(LA_ERR_INVALID_ARG, "window is negative");
   if (flags & ~LA_FLAG_SIMT) return fail(LA_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   if (((uintptr_t)lse) % 4) return fail(LA_ERR_INVALID_ARG, "lse not 4-byte aligned");

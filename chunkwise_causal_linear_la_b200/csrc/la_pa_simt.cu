@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_simt_kernel(const PagedArgs
   if (!locate(a.cu_seqlens, a.n_seqs, a.T, t, n, i, L)) return;
   const int64_t tb = a.cu_seqlens ? 0 : n, tt = a.cu_seqlens ? t : i;
   const T *q = (const T *)a.q.data + tb * a.q.sb + tt * a.q.st + h * a.q.sh;
-  for (int d = threadIdx.x; d < D; d += 32 * kWarps) sq[d] = to_f32<T>(q[d]) * a.scale;
+  for (int d = threadIdx.x; d < D; d += 32 * kWarps) sq[d] = to_f32<T>(q[d]);
   __syncthreads();
   const int64_t p = (int64_t)a.kv_len[n] - L + i;
   const int64_t cap = a.c.max_pages * (int64_t)a.c.page_size;
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_simt_kernel(const PagedArgs
 #pragma unroll
           for (int u = 0; u < 8; ++u) s = fmaf(f[u], sq[d + u], s);
         }
-        s *= ks;
+        s = s * ks * a.scale;  // last: a query times a large scale may leave fp32 where its score does not
       }
     }
     float mx = s;

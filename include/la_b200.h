@@ -616,7 +616,7 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  *   cache, page_table, max_pages, kv_len, cu_seqlens, n_seqs  as for la_kv_write.
  *               Positions past max_pages * page_size are not seen; a missing page
  *               inside the range is seen as rows of zeros.
- *   scale       positive factor of the scores (D^-1/2 usually).
+ *   scale       positive factor of the scores (D^-1/2 usually), at most 2.35e38.
  *   window      0, or the number of positions a query sees, itself included.
  *   out         written for every token that belongs to a sequence (others are
  *               left untouched); a query that sees nothing (p < 0) gives zeros.
@@ -652,7 +652,7 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  * a sequence's keys are split over CTAs depends on the whole call.
  *
  * Errors: as la_kv_write, and LA_ERR_INVALID_ARG for a scale that is not positive
- * and finite, a negative window, unknown flags; LA_ERR_WORKSPACE for a missing or
+ * or too large, a negative window, unknown flags; LA_ERR_WORKSPACE for a missing or
  * small workspace; LA_ERR_CUDA if a launch fails.
  */
 LA_API size_t la_paged_attn_workspace_size(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs,

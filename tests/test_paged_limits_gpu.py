@@ -114,3 +114,19 @@ def test_scores_that_are_all_minus_infinity(la, L, ctx, simt):
     assert bool((lse[0, :L, :2] == -math.inf).all()) and bool(torch.isnan(lse[0, :L, 2:]).all())
     assert bool((out[0, L:L + 2] == 0).all()) and bool((lse[0, L:L + 2] == -math.inf).all())
     assert bool(torch.isfinite(out[0, L + 2:]).all()) and bool(torch.isfinite(lse[0, L + 2:]).all())
+
+
+# --------------------------------------------------------------------- scales of the scores
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("simt", [False, True])
+def test_a_large_scale_and_large_queries(la, simt, dtype):
+    """A query element whose product with the scale is beyond fp32, on keys that are zero there, has no part."""
+    from test_paged_gpu import hold
+
+    c = Case([5], [60], 2, 2, 64, 16, BF, dtype=dtype, seed=3)
+    c.q = (c.q.double() * 2.0 ** -100).to(dtype)
+    c.q[:, :, 9] = 2.0 ** 50
+    c.k_rows[0][:, :, 9] = 0
+    scale = 2.0 ** 97
+    out, lse = attn(la, c, c.fill(la, "cuda"), scale=scale, flags=la.LA_FLAG_SIMT if simt else 0)
+    hold(c, out, lse, scale=scale, simt=simt or dtype != BF)
