@@ -1465,10 +1465,11 @@ bool pa_tc_supported(const PagedArgs &a) {
          !((a.B > 1 && a.q.sb == 0) || (a.T > 1 && a.q.st == 0) || (a.H > 1 && a.q.sh == 0));
 }
 
-// (size_t)-1 where the problem is too large for 32-bit entry numbers.
+// (size_t)-1 where the problem is too large: the plan adds two entry numbers in 32 bits, and multiplies the cost of all
+// entries (below 2^26 each: 2^24 key tiles, three for each) by the cache heads in 64.
 size_t pa_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs, bool packed, int64_t H_kv, int G) {
   const int64_t e = max_entries(B, T, n_seqs, packed, (int)(H / H_kv));
-  if (e > 0x7FFFFFF0) return (size_t)-1;
+  if (e > (int64_t)1 << 30 || e > ((int64_t)1 << 37) / H_kv) return (size_t)-1;
   return plan(e, n_seqs, (int)D, G).bytes;
 }
 
