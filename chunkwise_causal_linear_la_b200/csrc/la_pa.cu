@@ -76,11 +76,12 @@ using tcsync::Sync;
 // Bounded wait on a barrier: true once the phase has completed, false when the CTA has given up or this wait does (2^19
 // probes; one that fails sleeps for 7800 cycles: about two seconds), which is recorded.  It is kept short: it stands in
 // some thirty places, by warps that would share the instruction cache with the ones that work.
-__device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile) {
+constexpr uint32_t kProbes = 1u << 19;
+__device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity, int tile, uint32_t probes = kProbes) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
-      "mov.u32 n, 524288;\n"
+      "mov.u32 n, %4;\n"
       "AGAIN:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
       "ld.volatile.shared.u32 f, [%3];\n\t"
@@ -90,7 +91,7 @@ __device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(sy.bar + idx)), "r"(parity), "r"(smem_u32(const_cast<int *>(sy.abort)))
+      : "r"(smem_u32(sy.bar + idx)), "r"(parity), "r"(smem_u32(const_cast<int *>(sy.abort))), "r"(probes)
       : "memory");
   if (!ok && !*sy.abort) {
     *sy.abort = 1;
@@ -102,8 +103,9 @@ __device__ __forceinline__ bool wait_on(const Sync &sy, int idx, uint32_t parity
 __device__ __forceinline__ void arrive_n(uint64_t *bar, uint32_t n) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
-__device__ __forceinline__ bool wait_on_warp(const Sync &sy, int idx, uint32_t parity, int tile) {
-  return __all_sync(0xffffffffu, wait_on(sy, idx, parity, tile));
+__device__ __forceinline__ bool wait_on_warp(const Sync &sy, int idx, uint32_t parity, int tile,
+                                             uint32_t probes = kProbes) {
+  return __all_sync(0xffffffffu, wait_on(sy, idx, parity, tile, probes));
 }
 
 constexpr int kTile = 128;  // keys of a tile, rows of a query tile
@@ -1093,8 +1095,11 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       // ------------------------------------------------------------------ epilogue
       const float mc = m;
       const bool mine = two || w == 0;
+      // Warps without a row come here at once and wait for the whole item: 16 probes a key tile (60 us; one takes about
+      // two) on top.  (Where the CTA has stopped, the warps that wait for one tile give up first and end this one.)
+      const uint32_t probes = kProbes + 16 * it.n;
       if (!mine) {  // O[1] complete: the previous item's statistics have been read
-        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
+        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0, probes))) break;
         ++ocnt[1];
         if (lane < G::WROWS) ml[r] = make_float2(mc, l);
         __syncwarp();
@@ -1103,11 +1108,11 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         continue;
       }
       const bool join = !two;
-      if (!(ok = wait_on_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0))) break;
+      if (!(ok = wait_on_warp(sy, G::B_OFULL + w, ocnt[w] & 1, it.t0, probes))) break;
       ++ocnt[w];
       float M = mc, L = l, w0 = 1.f, w1 = 0.f;
       if (join) {
-        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0))) break;
+        if (!(ok = wait_on_warp(sy, G::B_OFULL + 1, ocnt[1] & 1, it.t0, probes))) break;
         if (!(ok = wait_on_warp(sy, G::B_MERGE, mcnt & 1, it.t0))) break;
         ++mcnt;
         const float2 o = ml[r];

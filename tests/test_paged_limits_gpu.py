@@ -130,3 +130,29 @@ def test_a_large_scale_and_large_queries(la, simt, dtype):
     scale = 2.0 ** 97
     out, lse = attn(la, c, c.fill(la, "cuda"), scale=scale, flags=la.LA_FLAG_SIMT if simt else 0)
     hold(c, out, lse, scale=scale, simt=simt or dtype != BF)
+
+
+# ------------------------------------------------------------------------------ long items
+def test_a_call_of_seconds(la):
+    """28 sequences of 2^31 - 2^16 positions each, all in one page: a CTA works more than three seconds on one entry, and its
+    warps without a row wait that long for its end.  The sum of the weights is the page's, once for each time it is
+    seen.  (A lane's own sum takes 3.2 million additions: off by 3.2e6 2^-24 = 0.19 at most, a logarithm by 0.21.)"""
+    n, page, pages = 28, 2 ** 16, 2 ** 15 - 1
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v, ks, vs = la.kv_cache(1, page, 1, 64, I8)
+    rows = torch.randn((1, page, 1, 64), generator=gen, device="cuda").to(BF)
+    one = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    la.la_kv_write(rows, torch.zeros_like(rows), k, v, one, torch.tensor([page], dtype=torch.int32, device="cuda"),
+                   k_scale=ks, v_scale=vs)
+    q = torch.randn((n, 1, 1, 64), generator=gen, device="cuda").to(BF)
+    out, lse = torch.full_like(q, math.nan), torch.full((n, 1, 1), math.nan, device="cuda")
+    table = torch.zeros((n, pages), dtype=torch.int32, device="cuda")
+    kl = torch.full((n,), page * pages, dtype=torch.int32, device="cuda")
+    assert la.device_error(reset=True) == (0, 0)
+    la.la_paged_attn(q, k, v, table, kl, k_scale=ks, v_scale=vs, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert la.device_error(reset=True) == (0, 0)
+    stored = la.la_kv_read(k, v, one, page, k_scale=ks, v_scale=vs, dtype=torch.float32)[0][0, :, 0].double()
+    want = torch.logsumexp(stored @ q[:, 0, 0].double().T / 8, 0) + math.log(pages)
+    assert bool(((lse[:, 0, 0].double() - want).abs() <= 0.21 + 1e-3).all())
+    assert bool((out == 0).all())
