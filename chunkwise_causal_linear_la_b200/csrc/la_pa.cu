@@ -1150,6 +1150,9 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
             for (int j = 0; j < 32; ++j) o[j] = w0 * o[j] + w1 * __uint_as_float(x[j]);
           }
           if (any_bad) {  // values that are not finite, for the queries that see them
+            // One bit a column: + and - infinity, both for NaN.  (A loop that is not unrolled, for its size: 32 conversions
+            // in a row here cost a call of many entries 8%, though they are not reached.)
+            uint32_t up = 0, down = 0;
             for (int t = it.t0; t < it.t0 + it.n; ++t) {
               const Reach rc = reach(a, it.e, t);
               if (!partly(rc)) continue;
@@ -1162,16 +1165,23 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                 const int sl = (int)((uint32_t)p - idx * (uint32_t)a.page_size);
                 const int64_t off = (int64_t)pg * a.s_page + (int64_t)sl * a.s_tok + (int64_t)it.head * a.s_head + 32 * q;
                 const float vs = G::Q8 ? a.vs[((int64_t)pg * a.Hkv + it.head) * a.page_size + sl] : 1.f;
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 32; ++u) {
                   float v;
                   if (FMT == LA_KV_BF16) v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.v)[off + u]);
                   else if (FMT == LA_KV_INT8) v = (float)(int8_t)a.v[off + u];
                   else v = __half2float(__half(__nv_cvt_fp8_to_halfraw(a.v[off + u], __NV_E4M3)));
                   if (G::Q8) v = __bfloat162float(__float2bfloat16_rn(v * vs));  // as the operand had it
-                  if (!finite_f(v)) o[u] += v;
+                  if (finite_f(v)) continue;
+                  if (!(v < 0.f)) up |= 1u << u;
+                  if (!(v > 0.f)) down |= 1u << u;
                 }
               }
+            }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              if (up >> u & 1) o[u] += INFINITY;
+              if (down >> u & 1) o[u] -= INFINITY;
             }
           }
           if (valid) {
@@ -1230,8 +1240,6 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       const int first = even ? ci * (TURNS / SET) : ((SET == 8 ? 0xDB917520u : 0xC720u) >> (4 * ci)) & 15;
       const int last = first + (even ? TURNS / SET : ((SET == 8 ? 0x32212231u : 0x4552u) >> (4 * ci)) & 15);
       for (int i = 0; i < it.n && ok; ++i) {
-        const Reach rc = reach(a, it.e, it.t0 + i);
-        const bool part = partly(rc);
         {
           if (!(ok = wait_on_warp(sy, G::B_RFULL + rs, rph, it.t0 + i))) break;
           if (!(ok = wait_on_warp(sy, G::B_EMPTY + os, oph, it.t0 + i))) break;
@@ -1248,16 +1256,6 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
               f[x] = D == 128 ? *reinterpret_cast<const float *>(reinterpret_cast<uintptr_t>(ss + u * 8) ^ (x * 8))
                               : ss[u * 16 + x * 8];
             }
-            if (part) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int row = D == 128 ? u * 8 + (r8 ^ (x * 2)) : u * 16 + x * 8 + r8;
-                if (row < rc.a || row >= rc.d) {  // seen by none, whatever it holds
-                  w[x] = make_uint4(0, 0, 0, 0);
-                  f[x] = 0.f;
-                }
-              }
-            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint4 o0, o1;
@@ -1267,24 +1265,25 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
               sts16(at ^ 16, o1);
             }
           }
-          // Values that some see: what is not finite is taken out, codes whose product with their scale leaves the range
-          // among it.  A second pass over what this lane has written, with the reach found anew: in the loop above, or with
-          // registers held for it, it costs single tokens 3% (one token over 1M, e4m3: 357 us so, 365 - 374).
-          if (part && kvi) {
-            int tile = it.t0 + i;
-            asm volatile("" : "+r"(tile));
-            const Reach rv = reach(a, it.e, tile);
+          // Values in rows that not every token sees (keys there are masked as scores): rows that none sees become zeros, and
+          // what is not finite in the others is taken out, products of codes and scales past the range too.  A second pass
+          // over what this lane has written: in the loop above it costs the tiles that need nothing of it.
+          if (kvi) {
+            const Reach rc = reach(a, it.e, it.t0 + i);
+            if (partly(rc)) {
 #pragma unroll 1
-            for (int u = 2 * first; u < 2 * last; ++u) {
-              const int x = u & 1, row = D == 128 ? (u >> 1) * 8 + (r8 ^ (x * 2)) : u * 8 + r8;
-              if (row >= rv.b && row < rv.c) continue;
-              const uint32_t at = D == 128 ? (dst + (u >> 1) * 1024) ^ (x * 0x120) : dst + u * 1024;
+              for (int u = 2 * first; u < 2 * last; ++u) {
+                const int x = u & 1, row = D == 128 ? (u >> 1) * 8 + (r8 ^ (x * 2)) : u * 8 + r8;
+                if (row >= rc.b && row < rc.c) continue;
+                const uint32_t at = D == 128 ? (dst + (u >> 1) * 1024) ^ (x * 0x120) : dst + u * 1024;
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint4 o = lds16(at ^ (16 * y));
-                if (take_out(o)) {
+                for (int y = 0; y < 2; ++y) {
+                  uint4 o = make_uint4(0, 0, 0, 0);
+                  if (row >= rc.a && row < rc.d) {
+                    o = lds16(at ^ (16 * y));
+                    found |= take_out(o);
+                  }
                   sts16(at ^ (16 * y), o);
-                  found = 1;
                 }
               }
             }
