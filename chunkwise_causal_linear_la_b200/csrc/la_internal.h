@@ -121,6 +121,7 @@ struct PagedArgs {  // la_paged_attn
   int H, dtype;
   float scale;
   int window;  // 0: none
+  bool test_wait_timeout = false;  // LA_FLAG_TEST_WAIT_TIMEOUT (tensor cores)
 };
 
 // Sets the calling thread's la_last_error() message and returns `status`.

@@ -23,6 +23,7 @@ la_status ok() { return report_error(LA_OK, ""); }
 
 bool head_dim_ok(int64_t d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
 
+constexpr int32_t kAttnFlags = LA_FLAG_SIMT | LA_FLAG_TEST_WAIT_TIMEOUT;
 constexpr int64_t kMaxElems = (int64_t)1 << 34;  // B T H D: 2^31 threads of eight elements
 
 // Positive sizes whose product stays within `most` (no overflow on the way).
@@ -188,7 +189,7 @@ int32_t la_paged_attn_path(int64_t H, int64_t D, int64_t H_kv, int64_t page_size
                            int32_t flags) {
   if (H <= 0 || H_kv <= 0 || H % H_kv || !head_dim_ok(D) || page_size <= 0 || page_size > 65536) return -1;
   if (format != LA_KV_BF16 && format != LA_KV_E4M3 && format != LA_KV_INT8) return -1;
-  if ((dtype != LA_F32 && dtype != LA_BF16) || (flags & ~LA_FLAG_SIMT)) return -1;
+  if ((dtype != LA_F32 && dtype != LA_BF16) || (flags & ~kAttnFlags)) return -1;
   return dtype == LA_BF16 && !(flags & LA_FLAG_SIMT) && pa_tc_shape(H, D, H_kv, page_size) ? 1 : 2;
 }
 
@@ -221,7 +222,7 @@ la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int3
   if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f))
     return fail(LA_ERR_INVALID_ARG, "scale must be positive and at most 2.35e38");
   if (window < 0) return fail(LA_ERR_INVALID_ARG, "window is negative");
-  if (flags & ~LA_FLAG_SIMT) return fail(LA_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (flags & ~kAttnFlags) return fail(LA_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   if (((uintptr_t)lse) % 4) return fail(LA_ERR_INVALID_ARG, "lse not 4-byte aligned");
   if (((uintptr_t)kv_len) % 4) return fail(LA_ERR_INVALID_ARG, "kv_len not 4-byte aligned");
   if (workspace && ((uintptr_t)workspace) % 256 != 0)
@@ -243,6 +244,7 @@ la_status la_paged_attn(const la_tensor *q, const la_kv_cache *cache, const int3
   a.n_seqs = n_seqs;
   a.H = (int)q->H;
   a.dtype = q->dtype;
+  a.test_wait_timeout = (flags & LA_FLAG_TEST_WAIT_TIMEOUT) != 0;
   a.scale = scale;
   a.window = window > 0x7FFFFFFF ? 0 : (int)window;  // positions are int32: a wider window hides nothing
   const size_t need = la_paged_attn_workspace_size(q->B, q->T, q->H, q->D, n_seqs, cu_seqlens != nullptr, cache->H,

@@ -124,7 +124,7 @@ struct PaArgs {
   const int32_t *cu, *kv_len, *table;
   int64_t T, max_pages, n_pages, n_seqs;
   int32_t page_size, box, g, tpt, per, Hkv, H, window;  // tokens of a query tile, of an entry
-  int32_t e_max, G;
+  int32_t e_max, G, test_stop;  // test_stop: LA_FLAG_TEST_WAIT_TIMEOUT
   int64_t cap;  // max_pages * page_size
   float c;      // scale * log2(e)
   void *out;
@@ -591,6 +591,10 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           const int pc = pg >= 0 ? pg : (int)a.n_pages;
 #pragma unroll
           for (int kvi = 0; kvi < 2; ++kvi, ++seq) {
+            if (kvi && a.test_stop) {  // no values: every role waits for them
+              ok = false;
+              break;
+            }
             const CUtensorMap *tm = kvi ? &tm_v : &tm_k;
             if (!G::Q8) {
               const int s = seq % G::NS;
@@ -632,19 +636,19 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           slot = nslot;
         }
       }
-      if (*abort_flag) {  // let every copy under way land before the CTA ends
-        if (lane == 0) {
-          constexpr uint32_t N = G::Q8 ? (G::NR > 0 ? G::NR : 1) : G::NS;
-          const int b = G::Q8 ? G::B_RFULL : G::B_FULL;
-          for (uint32_t s = seq > N ? seq - N : 0; s < seq; ++s) drain_bar(sy, b + s % N, (s / N) & 1);
-          if (items) drain_bar(sy, G::B_QFULL, (items - 1) & 1);
-        }
-        __syncwarp();
+      // Every copy under way lands before the CTA ends.  (Asked whether or not the CTA has given up yet: it may do so
+      // after this warp's last copies.)
+      if (lane == 0) {
+        constexpr uint32_t N = G::Q8 ? (G::NR > 0 ? G::NR : 1) : G::NS;
+        const int b = G::Q8 ? G::B_RFULL : G::B_FULL;
+        for (uint32_t s = seq > N ? seq - N : 0; s < seq; ++s) drain_bar(sy, b + s % N, (s / N) & 1);
+        if (items) drain_bar(sy, G::B_QFULL, (items - 1) & 1);
       }
+      __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       // The whole warp walks and waits, so that descriptors and addresses are uniform; one lane issues.
-        constexpr uint32_t ID_QK = idesc_bf16_f32(G::ROWS, kTile, 0, 0);
+      constexpr uint32_t ID_QK = idesc_bf16_f32(G::ROWS, kTile, 0, 0);
       constexpr uint32_t ID_PV = idesc_bf16_f32(G::ROWS, D, 0, 1);
       const uint64_t dq0 = smem_desc_sw128(smem_u32(sm + G::OFF_Q), 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(op_slot(0)), 16, 1024);
@@ -1499,6 +1503,7 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int G, void *workspace, cudaStre
   p.window = a.window;
   p.e_max = (int)max_entries(a.B, a.T, a.n_seqs, a.cu_seqlens != nullptr, g);
   p.G = G;
+  p.test_stop = a.test_wait_timeout;
   p.cap = a.c.max_pages * (int64_t)a.c.page_size;
   p.c = a.scale * 1.4426950408889634f;
   p.out = a.out;

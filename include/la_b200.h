@@ -66,12 +66,13 @@ typedef enum { LA_F32 = 0, LA_BF16 = 1 } la_dtype;
 /* Run the CUDA-core (SIMT, fp32 arithmetic) chunk kernel even where the
  * tensor-core kernel applies.  Both are CUDA kernels; there is no CPU path. */
 #define LA_FLAG_SIMT 1
-/* Testing the failure path, la_fwd_gated_delta_chunk on the tensor cores only:
- * the WY pass issues no tile load, so its first wait runs out (bounded: about
- * two seconds per CTA, plus as long again to drain), its CTAs raise their
- * abort flags, free their tensor memory and return; la_device_error then
- * reports the timeout (flags bit 0) and where it happened.  The call's
- * outputs are undefined; the CUDA context stays usable. */
+/* Testing the failure path, la_fwd_gated_delta_chunk and la_paged_attn on the
+ * tensor cores only: the first one's WY pass issues no tile load, the second
+ * one's CTAs load no values, so that waits run out (bounded: about two seconds
+ * per CTA, plus as long again to drain), the CTAs raise their abort flags, free
+ * their tensor memory and return; la_device_error then reports the timeout (flags
+ * bit 0) and where it happened.  The call's outputs are undefined; the CUDA
+ * context stays usable. */
 #define LA_FLAG_TEST_WAIT_TIMEOUT 0x100
 
 /*
@@ -621,7 +622,8 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  *   out         written for every token that belongs to a sequence (others are
  *               left untouched); a query that sees nothing (p < 0) gives zeros.
  *   lse         NULL, or device float[B, T, H]; -infinity where nothing is seen.
- *   flags       LA_FLAG_NONE, or LA_FLAG_SIMT for the CUDA-core kernel.
+ *   flags       LA_FLAG_NONE, or LA_FLAG_SIMT for the CUDA-core kernel;
+ *               LA_FLAG_TEST_WAIT_TIMEOUT (tests only).
  *   workspace   device scratch of at least la_paged_attn_workspace_size(...)
  *               bytes (NULL allowed when that is 0), 256-byte aligned; need not be
  *               initialised.  Calls whose work may overlap on the GPU (two streams,

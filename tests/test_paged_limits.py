@@ -27,3 +27,15 @@ def test_more_entries_than_the_plan_can_number_are_refused(lib):  # noqa: F811
     c = _c(fmt=0, k_scale=0, v_scale=0)
     assert lib.la_paged_attn(ctypes.byref(q), ctypes.byref(c), 0x100, 1, 0x200, 0x300, 0x7FFFFFE0, 0.1, 0,
                              ctypes.byref(out), None, 0, 0x100000, 1 << 62, None) == b.LA_ERR_UNSUPPORTED
+
+
+def test_the_failure_path_has_its_flag(lib):  # noqa: F811
+    from chunkwise_causal_linear_la_b200 import binding as b
+
+    t = b.LA_FLAG_TEST_WAIT_TIMEOUT
+    assert _attn(lib, flags=t) == b.LA_ERR_WORKSPACE  # taken: the next check speaks
+    assert b.paged_attn_path(16, 64, 4, 16, flags=t) == b.LA_PATH_TENSOR_CORE
+    assert b.paged_attn_path(16, 64, 4, 16, flags=t | b.LA_FLAG_SIMT) == b.LA_PATH_CUDA_CORE
+    assert b.paged_attn_path(16, 64, 4, 16, flags=t | 2) == -1 and _attn(lib, flags=t | 2) == b.LA_ERR_INVALID_ARG
+    assert b.paged_attn_workspace_size(1, 4, 4, 64, 1, False, 2, 16, flags=t) == b.paged_attn_workspace_size(
+        1, 4, 4, 64, 1, False, 2, 16)

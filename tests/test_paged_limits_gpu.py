@@ -156,3 +156,25 @@ def test_a_call_of_seconds(la):
     want = torch.logsumexp(stored @ q[:, 0, 0].double().T / 8, 0) + math.log(pages)
     assert bool(((lse[:, 0, 0].double() - want).abs() <= 0.21 + 1e-3).all())
     assert bool((out == 0).all())
+
+
+# ---------------------------------------------------------------------------- failure path
+@pytest.mark.parametrize("fmt,lens,ctx,D", [(BF, [1, 1], [3000, 200], 128), (E4, [1, 1], [3000, 200], 128),
+                                            (BF, [150, 40], [900, 0], 64), (I8, [150, 40], [900, 0], 128)])
+def test_waits_that_run_out_are_reported(la, fmt, lens, ctx, D):
+    """Failure detection without a GPU fault: with LA_FLAG_TEST_WAIT_TIMEOUT no CTA loads values, so its waits for them run
+    out after about two seconds; it lets its copies land, frees its tensor memory and returns.  la_device_error tells
+    of it, with no copy left under way, and the next calls are right.  One query tile and two, bf16 and 8 bits."""
+    from test_paged_gpu import hold
+
+    c = Case(lens, ctx, 8, 2, D, 16, fmt, seed=D)
+    cache = c.fill(la, "cuda")
+    assert la.device_error(reset=True) == (0, 0)
+    attn(la, c, cache, flags=la.LA_FLAG_TEST_WAIT_TIMEOUT)
+    torch.cuda.synchronize()
+    flags, where = la.device_error(reset=True)
+    assert flags == 1 and where >> 31 == 1, (flags, hex(where))
+    assert la.device_error(reset=True) == (0, 0)
+    for _ in range(2):
+        hold(c, *attn(la, c, cache))
+    assert la.device_error(reset=True) == (0, 0)
