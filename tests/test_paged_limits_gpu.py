@@ -99,6 +99,38 @@ def test_the_largest_rows_read_back_finite(la, fmt, dtype):
             assert bool(torch.isfinite(r).all())
 
 
+@pytest.mark.parametrize("fmt", [BF, E4, I8])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_codes_and_scales_of_values_as_of_keys(la, fmt, dtype):
+    """Keys and values of rows of every size, each with rows of its own that hold an infinity, a NaN, zeros, subnormal
+    numbers and ties: stored codes and scales are the formula's for both."""
+    dev = torch.device("cuda")
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn((2, 1, 40, 3, 32), generator=gen, dtype=torch.float64)
+    x *= torch.exp2(torch.randint(-140, 120, (2, 1, 40, 3, 1), generator=gen).double())
+    x[0, 0, 3], x[1, 0, 4] = 0, 0
+    x[0, 0, 5] = torch.arange(32) / 2.0
+    x[1, 0, 6] = -torch.arange(32) / 2.0
+    x = x.to(dtype)
+    x[0, 0, 7, 1, 9], x[1, 0, 8, 2, 0], x[0, 0, 9, 0, 31], x[1, 0, 10, 0, 5] = math.inf, math.nan, math.nan, -math.inf
+    k, v, ks, vs = la.kv_cache(3, 16, 3, 32, fmt)
+    table, kl = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=dev), torch.tensor([40], dtype=torch.int32, device=dev)
+    la.la_kv_write(x[0].to(dev), x[1].to(dev), k, v, table, kl, k_scale=ks, v_scale=vs)
+    for cache, scale, rows in ((k, ks, x[0, 0]), (v, vs, x[1, 0])):
+        got = cache[table[0].long()].reshape(48, 3, 32)[:40].cpu() if fmt != E4 else (
+            cache.view(torch.int8)[table[0].long()].reshape(48, 3, 32)[:40].cpu().view(E4))
+        if fmt == BF:
+            want = rows.to(BF)
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+            continue
+        s = scale[table[0].long()].transpose(1, 2).reshape(48, 3)[:40].cpu().double()
+        bad = ~torch.isfinite(rows).all(-1)
+        assert int(bad.sum()) == 2 and torch.equal(torch.isnan(s), bad)
+        code, want = quantise(torch.where(bad[..., None], 0.0, rows.double()), fmt)
+        assert torch.equal(got.float().double(), code)
+        assert torch.equal(s[~bad], want[..., 0][~bad])
+
+
 # ----------------------------------------------------------- scores that are all -infinity
 @pytest.mark.parametrize("simt", [False, True])
 @pytest.mark.parametrize("L,ctx", [(1, 20), (9, 100), (70, 300), (1, 20000)])
@@ -178,3 +210,63 @@ def test_waits_that_run_out_are_reported(la, fmt, lens, ctx, D):
     for _ in range(2):
         hold(c, *attn(la, c, cache))
     assert la.device_error(reset=True) == (0, 0)
+
+
+# --------------------------------------------------------------------------- repeated calls
+@pytest.mark.parametrize("fmt", [BF, E4, I8])
+@pytest.mark.parametrize("lens,ctx,H,Hkv,D,page,window", [
+    ([1] * 33, [131 * (i % 9) + 29 * i for i in range(33)], 8, 2, 128, 16, 0),
+    ([1], [30000], 8, 2, 128, 64, 0),
+    ([5] * 7, [300 * i for i in range(7)], 16, 16, 64, 16, 0),
+    ([1, 200, 1, 77], [4000, 700, 127, 2500], 10, 2, 128, 32, 0),
+    ([300, 140], [1800, 900], 8, 2, 64, 48, 300),
+])
+def test_the_same_call_gives_the_same_bits(la, lens, ctx, H, Hkv, D, page, window, fmt):
+    """Nothing of a result depends on the order in which CTAs or warps come: thirty calls agree bit by bit, with
+    workspaces of different content and other calls in between."""
+    c = Case(lens, ctx, H, Hkv, D, page, fmt, seed=D + len(lens))
+    cache = c.fill(la, "cuda")
+    other = Case([1, 60], [700, 40], 8, 2, 64, 16, I8, seed=2)
+    other_cache = other.fill(la, "cuda")
+    first = attn(la, c, cache, window=window)
+    need = la.paged_attn_workspace_size(1, sum(lens), H, D, len(lens), True, Hkv, page, fmt)
+    for i in range(30):
+        if i % 3 == 0:
+            attn(la, other, other_cache)
+        ws = torch.full((need,), 37 * i % 256, dtype=torch.uint8, device="cuda")
+        out, lse = attn(la, c, cache, window=window, workspace=ws)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), i
+
+
+def test_two_streams_agree_with_themselves(la):
+    """Every one of many calls on two streams at once gives what the same call gives by itself."""
+    cases = [Case([1, 60], [700, 40], 8, 2, 64, 16, BF, seed=1), Case([1, 60, 1], [2700, 40, 9], 8, 2, 128, 16, I8, seed=2)]
+    caches = [c.fill(la, "cuda") for c in cases]
+    alone = [attn(la, c, cache) for c, cache in zip(cases, caches)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(50):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(attn(la, cases[i], caches[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+
+
+@pytest.mark.parametrize("fmt", [BF, I8])
+def test_a_cache_without_pages(la, fmt):
+    """Every page is missing: rows of zeros, so zeros with the logarithm of the number of positions; writes go nowhere."""
+    dev = torch.device("cuda")
+    k, v, ks, vs = la.kv_cache(0, 16, 2, 64, fmt)
+    table, kl = torch.full((1, 4), 3, dtype=torch.int32, device=dev), torch.tensor([40], dtype=torch.int32, device=dev)
+    q = torch.randn(1, 5, 4, 64, device=dev).to(BF)
+    la.la_kv_write(q[:, :, :2], q[:, :, 2:], k, v, table, kl, k_scale=ks, v_scale=vs)
+    out, lse = la.la_paged_attn(q, k, v, table, kl, k_scale=ks, v_scale=vs, return_lse=True)
+    assert bool((out == 0).all())
+    want = torch.log(torch.arange(36, 41).double())[:, None].expand(5, 4)
+    assert bool(((lse[0].double().cpu() - want).abs() <= 40 * 2.0 ** -23 + 2.0 ** -20).all())
+    r = la.la_kv_read(k, v, table, 8, k_scale=ks, v_scale=vs)
+    assert bool((r[0] == 0).all()) and bool((r[1] == 0).all())
