@@ -12,10 +12,12 @@
 // row, each with 16 bytes of its dense side, keys and values of one row in one
 // thread so that two loads are in flight, and the row's maximum goes through
 // shuffles.  Measured for 16 sequences of up to 16384 tokens, 8 heads of 128, against
-// the rate of a plain copy: bf16 written 203 us (94%), read 206 us (93%); e4m3 216 us
-// (67%), 179 us (81%); int8 215 us (67%), 172 us (84%).  The 8-bit forms are held
-// by their instructions (two thirds of the issue slots; conversions at half rate and
-// less) beside memory.
+// the rate of a plain copy (one call by itself; an 8-bit read among others 176 us):
+//   bf16 rows: bf16 written 203 us (94%), read 206 (93%); e4m3 212 (68%), 179 (81%); int8 212 (68%), 173 (84%)
+//   f32 rows:  bf16 written 302 us (95%), read 322 (89%); e4m3 260 (93%), 281 (86%); int8 260 (92%), 282 (85%)
+// 8-bit reads and writes of bf16 rows leave both memory (49% in a read of 64 prompts,
+// under the profiler) and issue slots (65%) free: a block's turns follow one another,
+// loads, maxima, stores.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

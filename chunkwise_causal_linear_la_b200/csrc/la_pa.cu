@@ -39,17 +39,22 @@
 // scores are masked by selection, but 0 * inf in PV would be NaN.  Rows that no query
 // of the entry sees are zeroed; in rows that some see, values that are not finite
 // are taken out of the operand and added at the end for the queries that see them.
+// (8-bit caches: by the converted values, since a code times a finite scale may be
+// infinite too.)
 //
 // Every wait is bounded: on a timeout the CTA records it, drains and returns.
 //
-// What bounds it, measured on one B200 (bf16 unless said, 8 cache heads of 128):
-//   2048 tokens over 16384, 32 heads     254 us (275 back to back, at the power limit), 1.01 PFLOP/s (61% of the
+// What bounds it, measured on one B200 (bf16 unless said, 16 query heads over 4 cache heads of 128):
+//   2048 tokens over 16384               247 us (275 back to back, at the power limit), 1.04 PFLOP/s (63% of the
 //                                        library's matrix product): a softmax group's chain (scores in, exponentials,
-//                                        P out) beside its products; tensor pipe 54%
-//   256 single tokens over up to 8192    342 us (356 back to back), 6.3 TB/s (97% of a copy): memory
-//   one token over 1,048,576, e4m3       357 us, 3.1 TB/s: conversion of codes (244 us without it, 240 without the
-//                                        softmax's work too; its instructions alone would take 1060 of 2980 cycles a tile)
-//   44 tokens and 4 pieces, e4m3         197 us: a new entry costs a CTA 4 - 6 us beside its key tiles
+//                                        P out) beside its products; tensor pipe 53%
+//   the same, e4m3 and int8              350 and 367 us: 3.4 and 3.5 us a key tile of a CTA where bf16 takes 2.3 (one
+//                                        stage of codes each for keys and values, eight conversion warps, spills)
+//   256 single tokens over up to 8192    342 us (353 back to back), 6.3 TB/s (97% of a copy): memory
+//   one token over 1,048,576, e4m3       334 us (343 back to back), 3.3 TB/s: conversion of codes (244 us without it, 240
+//                                        without the softmax's work too)
+//   44 tokens and 4 pieces, e4m3,        179 us: 43 key tiles a CTA as above; its two entries cost it 4 - 6 us each
+//   20 query heads                       beside them
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -180,7 +185,8 @@ __device__ __forceinline__ void seq_span(const PaArgs &a, int64_t n, int64_t &st
 }
 
 // What a key tile and an entry cost a CTA, in thirds of a tile of two query tiles (about 2 us; one query tile: 1.4 us).
-// An entry costs about two tiles besides its own: its queries' way in, the first weights, its results.
+// An entry costs about two tiles besides its own: its queries' way in, the first weights, its results.  (As bf16 with
+// heads of 128 measured; used for every form.  In 8 bits a two-tile one takes 3.4 us.)
 __device__ __forceinline__ int tile_cost(const PaArgs &a, const Entry &e) { return e.ntok > a.tpt ? 3 : 2; }
 __device__ __forceinline__ int64_t entry_cost(const PaArgs &a, const Entry &e) {
   return (int64_t)tile_cost(a, e) * e.cnt + (e.ntok > a.tpt ? 6 : 3);
@@ -1155,7 +1161,7 @@ pa_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           }
           if (any_bad) {  // values that are not finite, for the queries that see them
             // One bit a column: + and - infinity, both for NaN.  (A loop that is not unrolled, for its size: 32 conversions
-            // in a row here cost a call of many entries 8%, though they are not reached.)
+            // in a row here cost a call of many entries 7%, though they are not reached.)
             uint32_t up = 0, down = 0;
             for (int t = it.t0; t < it.t0 + it.n; ++t) {
               const Reach rc = reach(a, it.e, t);
@@ -1391,8 +1397,15 @@ int box_rows(int64_t page_size) {  // largest power of two that divides the page
 
 // Query tiles of an entry: one of 64 rows where the sequences have no more rows each on average (single tokens, drafts:
 // the two softmax groups take half of each key tile, and shared memory goes to more of those), else two of 128 (they
-// share the keys).  Measured with 64 rows and with 128 for single tokens: 256 over up to 8192 (bf16) 344 and 469 us.
-// Prompts need the shared keys: a CTA that reads 64 rows' worth of keys does a quarter of the products for them.
+// share the keys).  Measured with 64 rows and with 128, 16 heads over 4 of 128:
+//   256 single tokens over up to 8192    bf16 334 and 360 us, e4m3 349 and 475, int8 394 and 524
+//   2048 tokens over 16384               bf16 456 and 247 us, e4m3 569 and 350, int8 668 and 367: a CTA that reads 64
+//                                        rows' worth of keys does a quarter of the products for them
+// The average decides for a whole call, since lengths are known to the device only.  Calls of both kinds:
+//   256 single tokens, a piece of 2048   (64 is taken) bf16 434 and 454 us, e4m3 547 and 606, int8 625 and 646; as two
+//                                        calls 444, 498 and 547
+//   44 single tokens, 4 pieces           (128 is taken) bf16 174 and 138 us, e4m3 203 and 182, int8 223 and 193; as two
+//   of 200 to 512, 20 heads over 4       calls 147, 175 and 191
 int query_tiles(int64_t B, int64_t T, int64_t n_seqs, bool packed, int g) {
   const int64_t tokens = packed ? T : B * T;
   return g <= 64 && tokens <= n_seqs * tokens_per_tile(g, 1) ? 1 : 2;

@@ -8,8 +8,8 @@
 // its own (the row is one or a few 32-byte sectors), then the lanes turn to the
 // value columns and each key's weight goes round by a shuffle.  Positions that are
 // not seen are not read.  All arithmetic is fp32; the keys' reads are not
-// coalesced, which bounds it (2048 tokens over 16384, 32 heads of 128: 86 ms, 3
-// TFLOP/s; the tensor cores' form takes 0.25): it is the form that is right for every
+// coalesced, which bounds it (2048 tokens over 16384, 16 heads of 128 over 4: 86 ms,
+// 3 TFLOP/s; the tensor cores' form takes 0.25): it is the form that is right for every
 // shape, not the one that serves.
 #include <cuda_bf16.h>
 #include <math.h>

@@ -540,7 +540,7 @@ LA_API la_status la_bwd_chunk_gated_norm(const la_tensor *q, const la_tensor *k,
 
 /* How a cache holds a row (the D values of one token and head).  The 8-bit
  * formats keep one scale per row, a power of two, so that code * scale is exact
- * in bf16: s = 2^e, the smallest with max |x| <= qmax s and e >= -126, and
+ * in bf16 (above 2^-133, its smallest number): s = 2^e, the smallest with max |x| <= qmax s and e >= -126, and
  * code = x / s rounded to nearest even (qmax 448 for e4m3, 127 for int8; e4m3
  * without infinities, as NVIDIA and OCP define it); a code whose product with s
  * would be 2^128 (rows above 1.93 2^127) is the next one towards zero, so that
@@ -642,20 +642,24 @@ LA_API la_status la_kv_read(const la_kv_cache *cache, const int32_t *page_table,
  * address: no value of theirs makes the call read or write out of bounds.
  *
  * Kernels: bf16 with D 64 or 128, page_size a multiple of 8, at most 128 query
- * heads a cache head and q strides that are not zero run on the tensor cores;
- * every other shape, f32 and LA_FLAG_SIMT on the CUDA cores, in fp32 (tens of times
- * slower).  la_paged_attn_path tells (as la_fwd_chunk_path does; -1: rejected).
+ * heads a cache head, q strides that are not zero and a cache that has pages run on
+ * the tensor cores; every other shape, f32 and LA_FLAG_SIMT on the CUDA cores, in
+ * fp32 (tens of times slower).  la_paged_attn_path tells (as la_fwd_chunk_path does;
+ * -1: rejected) from the shape: not from strides and the number of pages.
  *
  * Arithmetic: 8-bit rows enter as the values they stand for, on the tensor cores
  * rounded to bf16 (which changes nothing where scales are powers of two); scores,
  * softmax statistics and outputs are accumulated in fp32; on the tensor cores the
  * softmax weights are rounded to bf16 for the product with v; out is rounded once.
+ * The weighted values are summed before the division, weights up to 2^8: values
+ * times 2^8 times the keys that are seen have to stay inside fp32's range.
  * Results do not depend on other sequences of the call beyond fp32 rounding: where
  * a sequence's keys are split over CTAs depends on the whole call.
  *
  * Errors: as la_kv_write, and LA_ERR_INVALID_ARG for a scale that is not positive
- * or too large, a negative window, unknown flags; LA_ERR_WORKSPACE for a missing or
- * small workspace; LA_ERR_CUDA if a launch fails.
+ * or too large, a negative window, unknown flags; LA_ERR_UNSUPPORTED for more than
+ * 2^30 sequences and groups of rows; LA_ERR_WORKSPACE for a missing or small
+ * workspace; LA_ERR_CUDA if a launch fails.
  */
 LA_API size_t la_paged_attn_workspace_size(int64_t B, int64_t T, int64_t H, int64_t D, int64_t n_seqs,
                                            int32_t has_cu_seqlens, int64_t H_kv, int64_t page_size,
