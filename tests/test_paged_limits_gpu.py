@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from paged_util import Case, quantise
+from paged_util import Case, attend, bounds, quantise
 
 pytestmark = pytest.mark.gpu
 E4, I8, BF = torch.float8_e4m3fn, torch.int8, torch.bfloat16
@@ -270,3 +270,53 @@ def test_a_cache_without_pages(la, fmt):
     assert bool(((lse[0].double().cpu() - want).abs() <= 40 * 2.0 ** -23 + 2.0 ** -20).all())
     r = la.la_kv_read(k, v, table, 8, k_scale=ks, v_scale=vs)
     assert bool((r[0] == 0).all()) and bool((r[1] == 0).all())
+
+
+# ---------------------------------------------------------------------- beside a linear layer
+@pytest.mark.parametrize("fmt", [BF, E4, I8])
+def test_a_linear_layer_and_a_softmax_layer_over_one_batch(la, oracle_mod, fmt):
+    """As a hybrid stack runs: a linear-attention layer's outputs are the next layer's queries, keys and values, first for two
+    packed prompts (la_fwd_chunk, then la_kv_write and la_paged_attn), then token by token (la_step on the first
+    layer's states).  The first layer against the oracle, the second against the formula over the rows that the first
+    one gave."""
+    from parity_util import TOL, slice_rel_err, to_np
+
+    dev, gen = torch.device("cuda"), torch.Generator().manual_seed(9)
+    lens, steps, H, D, page = [150, 70], 6, 4, 64, 16
+    gamma = torch.tensor([0.9, 0.95, 0.99, 0.999])
+    x = [[(torch.randn((1, n + steps, H, D), generator=gen) * s).to(BF) for s in (D ** -0.5, 1.0, 0.3)] for n in lens]
+    cu = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device=dev)
+    k, v, ks, vs = la.kv_cache(32, page, 2, D, fmt)
+    table = torch.randperm(32, generator=gen).to(torch.int32).reshape(2, 16)[:, :12].contiguous().to(dev)
+    sc = dict(k_scale=ks, v_scale=vs)
+
+    def softmax_layer(o, kv_len, cu_seqlens):
+        kl = torch.tensor(kv_len, dtype=torch.int32, device=dev)
+        la.la_kv_write(o[:, :, :2], o[:, :, 2:], k, v, table, kl, cu_seqlens=cu_seqlens, **sc)
+        return la.la_paged_attn(o, k, v, table, kl, cu_seqlens=cu_seqlens, return_lse=True, **sc)
+    q0, k0, v0 = (torch.cat([x[n][i][:, :lens[n]] for n in range(2)], 1).to(dev) for i in range(3))
+    o, state = la.la_fwd_chunk(q0, k0, v0, gamma.to(dev), cu_seqlens=cu)
+    p, lse = softmax_layer(o, lens, cu)
+    first = [[o[0, :lens[0]]], [o[0, lens[0]:]]]
+    second = [[(p[0, :lens[0]], lse[0, :lens[0]])], [(p[0, lens[0]:], lse[0, lens[0]:])]]
+    for t in range(steps):
+        one = [torch.cat([x[n][i][:, lens[n] + t] for n in range(2)]).to(dev) for i in range(3)]  # [2, H, D]
+        o = la.la_step(one[0], one[1], one[2], gamma.to(dev), state)
+        p, lse = softmax_layer(o[:, None], [n + t + 1 for n in lens], None)
+        for n in range(2):
+            first[n].append(o[n][None])
+            second[n].append((p[n], lse[n]))
+    for n in range(2):
+        S = lens[n] + steps
+        o = torch.cat(first[n])
+        ref, _ = oracle_mod.recurrent(*x[n], gamma.tolist())
+        assert slice_rel_err(to_np(o[None]), ref, [(0, 0, S)]) < TOL[BF]
+        rows = o.cpu().double()
+        stored = [rows[:, :2], rows[:, 2:]]
+        if fmt != BF:
+            stored = [c * s for c, s in (quantise(r, fmt) for r in stored)]
+        want, wl, a, big = attend(rows, *stored, 0, 0, D ** -0.5)
+        tol, ltol = bounds(want, wl, a, big, S, D, BF, True)
+        got, gl = (torch.cat([y[i] for y in second[n]]).double().cpu() for i in range(2))
+        assert bool(((got - want).abs() <= tol).all()) and bool(((gl - wl).abs() <= ltol).all())
+    assert la.device_error(reset=True) == (0, 0)
